@@ -27,6 +27,8 @@ __all__ = [
     "status_string",
     "set_kernel_events",
     "attention", "EXPORTED",
+    "qk_norm_rope", "qk_norm_rope_fwd", "qk_norm_rope_bwd", "rope_tables", "cache_append", "cache_read",
+    "decode_paged_fp8", "decode_fp8_workspace_size",
 ]
 
 FA_BF16 = 0
@@ -41,7 +43,8 @@ EXPORTED = ("fa_fwd", "fa_bwd_workspace_size", "fa_bwd", "fa_status_string", "fa
             "fa_fwd_window", "fa_bwd_window", "fa_fwd_fp8",
             "fa_fwd_blocksparse", "fa_bwd_blocksparse", "fa_merge_partial", "fa_accumulate_bf16",
             "fa_cast_bf16", "fa_bwd_workspace_size_gqa", "fa_decode_paged", "fa_decode_workspace_size",
-            "fa_fwd_fp8_blocksparse")
+            "fa_fwd_fp8_blocksparse", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd", "fa_qk_norm_rope_workspace_size",
+            "fa_cache_append", "fa_cache_read", "fa_decode_paged_fp8", "fa_decode_fp8_workspace_size")
 # Test-only symbols (csrc/fa_testing.h): the first in libfa.so, the others in the
 # separate test library libfa_probe.so.
 TESTING_EXPORTED = {"libfa.so": ("fa_debug_inject",),
@@ -115,6 +118,20 @@ def lib() -> ctypes.CDLL:
     L.fa_decode_paged.restype = i
     L.fa_decode_workspace_size.argtypes = [i, i, i, i, i, i]
     L.fa_decode_workspace_size.restype = sz
+    L.fa_qk_norm_rope.argtypes = [vp] * 9 + [i] * 5 + [vp, vp, i, f, i, i, i, vp]
+    L.fa_qk_norm_rope.restype = i
+    L.fa_qk_norm_rope_bwd.argtypes = [vp] * 13 + [i] * 5 + [vp] * 4 + [i, f, i, i, i, vp, sz, vp]
+    L.fa_qk_norm_rope_bwd.restype = i
+    L.fa_qk_norm_rope_workspace_size.argtypes = [i]
+    L.fa_qk_norm_rope_workspace_size.restype = sz
+    L.fa_cache_append.argtypes = [vp] * 8 + [i] * 4 + [vp, vp, i, i, i, i, vp]
+    L.fa_cache_append.restype = i
+    L.fa_cache_read.argtypes = [vp] * 7 + [i] * 8 + [vp]
+    L.fa_cache_read.restype = i
+    L.fa_decode_paged_fp8.argtypes = [vp] * 8 + [i] * 7 + [f, i, vp, sz, vp]
+    L.fa_decode_paged_fp8.restype = i
+    L.fa_decode_fp8_workspace_size.argtypes = [i] * 7
+    L.fa_decode_fp8_workspace_size.restype = sz
     L.fa_status_string.argtypes = [i]
     L.fa_status_string.restype = ctypes.c_char_p
     L.fa_last_cuda_error.argtypes = []
@@ -530,3 +547,343 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None, window=
     """Differentiable attention: q [B, N, H, d], k and v [B, N, Hkv, d] (Hkv divides H);
     optional sliding ``window`` = (left, right) and 128 x 128 ``block_mask``."""
     return _Attention.apply(q, k, v, causal, scale, window, block_mask)
+
+
+# --------------------------------------------------------------------------
+# Around the attention: norm and rotation of query and key heads, the paged cache
+# --------------------------------------------------------------------------
+def _launch(device, stream, call):
+    """``call(handle)`` with ``device`` current and what it allocates taken from the stream that the kernels run on
+    (so that the memory of a temporary is only handed out again behind them)."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return call(torch.cuda.current_stream().cuda_stream)
+    if stream is not None and stream.device != device:
+        raise ValueError("stream belongs to another device than the tensors")
+    with torch.cuda.device(device):
+        if stream is None:
+            return call(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+
+
+def _strides(t, name):
+    """None for a dense [B, N, heads, d] tensor, else its (batch, position, head) strides for the C call."""
+    if t.is_contiguous():
+        return None
+    sb, sn, sh, sd = t.stride()
+    if t.numel() == 0:
+        return None
+    if sd != 1:
+        raise ValueError(f"{name}: the features of a head must be contiguous")
+    B, N, h, _ = t.shape
+    s = (sb if B > 1 else 0, sn if N > 1 else 0, sh if h > 1 else 0)
+    unit = 16 // t.element_size()
+    if any(x % unit for x in s):
+        raise ValueError(f"{name}: strides must be multiples of 16 bytes")
+    return (ctypes.c_longlong * 3)(*s)
+
+
+def _out_like(out, shape, dtype, device, name):
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if out.shape != torch.Size(shape) or out.dtype != dtype or out.device != device or not out.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return out
+
+
+def _rope_check(q, k, cos, sin, q_weight, k_weight, positions):
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("expected q [B, N, H, d] and k [B, N, Hkv, d]")
+    B, N, H, d = q.shape
+    if k.shape[0] != B or k.shape[1] != N or k.shape[3] != d:
+        raise ValueError("q and k must agree in batch, positions and head dim")
+    dtype = _dtype_code(q)
+    if k.dtype != q.dtype:
+        raise TypeError("q and k must have one dtype")
+    if cos.dtype != torch.float32 or sin.dtype != torch.float32:
+        raise TypeError("cos and sin must be float32")
+    if cos.dim() != 2 or cos.shape[1] * 2 != d or sin.shape != cos.shape:
+        raise ValueError("cos and sin must be [positions, d / 2] tables")
+    if not (cos.is_contiguous() and sin.is_contiguous()):
+        raise ValueError("cos and sin must be contiguous")
+    if (q_weight is None) != (k_weight is None):
+        raise ValueError("give both gains or none")
+    wdtype = dtype
+    others = [k, cos, sin]
+    if q_weight is not None:
+        wdtype = _dtype_code(q_weight)
+        if k_weight.dtype != q_weight.dtype:
+            raise TypeError("q_weight and k_weight must have one dtype")
+        if q_weight.shape != (d,) or k_weight.shape != (d,):
+            raise ValueError("q_weight and k_weight must be [d]")
+        if not (q_weight.is_contiguous() and k_weight.is_contiguous()):
+            raise ValueError("q_weight and k_weight must be contiguous")
+        others += [q_weight, k_weight]
+    if positions is None:
+        if N > cos.shape[0] and B > 0:
+            raise ValueError("the tables have fewer rows than there are positions")
+    else:
+        if positions.dtype != torch.int32:
+            raise TypeError("positions must be int32")
+        if positions.shape != (B, N) or not positions.is_contiguous():
+            raise ValueError("positions must be a contiguous [B, N] tensor")
+        others.append(positions)
+    for t in others:
+        if t.device != q.device:
+            raise ValueError("all tensors must share one device")
+    if not q.is_cuda:
+        raise ValueError("tensors must live on a CUDA device (there is no CPU path)")
+    return B, N, H, k.shape[2], d, dtype, wdtype
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def rope_tables(positions: int, d: int, base: float = 10000.0, device="cuda"):
+    """The (cos, sin) tables [positions, d / 2] fp32 that ``qk_norm_rope`` reads, for the angles p * base^(-2i/d).
+    Set up once: angles and functions are computed in float64 with PyTorch, so far positions are right."""
+    freq = float(base) ** (-torch.arange(0, d, 2, dtype=torch.float64, device=device) / d)
+    angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * freq
+    return angle.cos().float(), angle.sin().float()
+
+
+def qk_norm_rope_fwd(q, k, cos, sin, q_weight=None, k_weight=None, positions=None, eps: float = 1e-6,
+                     interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """RMS norm of every query and key head and the rotation by position (fa_qk_norm_rope): returns
+    (q_out [B, N, H, d], k_out [B, N, Hkv, d]), ready for ``fwd`` and ``cache_append``.
+
+    q, k: bf16 or fp32, also strided views (slices of a packed projection).
+    ``cos``, ``sin``: [positions, d / 2] fp32 tables (``rope_tables``).
+    ``q_weight``, ``k_weight``: [d] gains, or None for the rotation alone.
+    ``positions``: [B, N] int32 (negative: padding, a zero row), None: 0 .. N - 1.
+    ``interleaved``: pairs (2i, 2i + 1) instead of (i, i + d / 2).
+    """
+    B, N, H, Hkv, d, dt, wdt = _rope_check(q, k, cos, sin, q_weight, k_weight, positions)
+    qs, ks = _strides(q, "q"), _strides(k, "k")
+
+    def call(handle):
+        qo = _out_like(q_out, (B, N, H, d), q.dtype, q.device, "q_out")
+        ko = _out_like(k_out, (B, N, Hkv, d), q.dtype, q.device, "k_out")
+        rc = lib().fa_qk_norm_rope(q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), cos.data_ptr(),
+                                   sin.data_ptr(), _ptr(positions), qo.data_ptr(), ko.data_ptr(), B, N, H, Hkv, d, qs,
+                                   ks, cos.shape[0], eps, 1 if interleaved else 0, dt, wdt, handle)
+        if rc != 0:
+            raise FAError(rc, "fa_qk_norm_rope")
+        return qo, ko
+
+    return _launch(q.device, stream, call)
+
+
+def qk_norm_rope_bwd(q, k, cos, sin, dq_out, dk_out, q_weight=None, k_weight=None, positions=None, eps: float = 1e-6,
+                     interleaved: bool = False, workspace=None, stream=None):
+    """Backward of ``qk_norm_rope_fwd`` (fa_qk_norm_rope_bwd): from the gradients of its outputs returns
+    (dq, dk, dq_weight, dk_weight); the last two are None without gains.  ``workspace``: a uint8 tensor of
+    fa_qk_norm_rope_workspace_size bytes, to avoid the allocation."""
+    B, N, H, Hkv, d, dt, wdt = _rope_check(q, k, cos, sin, q_weight, k_weight, positions)
+    for g, x, name in ((dq_out, q, "dq_out"), (dk_out, k, "dk_out")):
+        if g.shape != x.shape or g.dtype != x.dtype or g.device != x.device:
+            raise ValueError(f"{name} must have the shape, dtype and device of its output")
+    if workspace is not None and (workspace.device != q.device or not workspace.is_contiguous()):
+        raise ValueError("workspace must be contiguous, on the device of q")
+    st = [_strides(t, n) for t, n in ((q, "q"), (k, "k"), (dq_out, "dq_out"), (dk_out, "dk_out"))]
+
+    def call(handle):
+        dq = torch.empty((B, N, H, d), dtype=q.dtype, device=q.device)
+        dk = torch.empty((B, N, Hkv, d), dtype=q.dtype, device=q.device)
+        dwq = dwk = ws = None
+        size = 0
+        if q_weight is not None:
+            dwq, dwk = torch.empty_like(q_weight), torch.empty_like(k_weight)
+            size = int(lib().fa_qk_norm_rope_workspace_size(d))
+            ws = torch.empty(max(size, 1), dtype=torch.uint8, device=q.device) if workspace is None else workspace
+            size = ws.numel() * ws.element_size()
+        rc = lib().fa_qk_norm_rope_bwd(q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), cos.data_ptr(),
+                                       sin.data_ptr(), _ptr(positions), dq_out.data_ptr(), dk_out.data_ptr(),
+                                       dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), B, N, H, Hkv, d, *st,
+                                       cos.shape[0], eps, 1 if interleaved else 0, dt, wdt, _ptr(ws), size, handle)
+        if rc != 0:
+            raise FAError(rc, "fa_qk_norm_rope_bwd")
+        return dq, dk, dwq, dwk
+
+    return _launch(q.device, stream, call)
+
+
+def _readable(g):
+    """An incoming gradient as the kernels read it: features contiguous, 16-byte strides and base."""
+    unit = 16 // g.element_size()
+    sb, sn, sh, sd = g.stride()
+    if sd == 1 and sb % unit == 0 and sn % unit == 0 and sh % unit == 0 and g.data_ptr() % 16 == 0:
+        return g
+    return g.contiguous()
+
+
+class _QKNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
+        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
+        ctx.eps, ctx.interleaved = eps, interleaved
+        return qk_norm_rope_fwd(q, k, cos, sin, q_weight, k_weight, positions, eps, interleaved)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        q, k, q_weight, k_weight, cos, sin, positions = ctx.saved_tensors
+        dq, dk, dwq, dwk = qk_norm_rope_bwd(q, k, cos, sin, _readable(dq_out), _readable(dk_out), q_weight, k_weight,
+                                            positions, ctx.eps, ctx.interleaved)
+        return dq, dk, dwq, dwk, None, None, None, None, None
+
+
+def qk_norm_rope(q, k, cos, sin, q_weight=None, k_weight=None, positions=None, eps: float = 1e-6,
+                 interleaved: bool = False):
+    """Differentiable ``qk_norm_rope_fwd`` (gradients of q, k and the gains; the tables get none): the step before
+    ``attention``."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k, q_weight, k_weight)):
+        return _QKNormRope.apply(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+    return qk_norm_rope_fwd(q, k, cos, sin, q_weight, k_weight, positions, eps, interleaved)
+
+
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+_SCALES = (torch.uint8, torch.float8_e8m0fnu)
+
+
+def _cache_check(k_cache, v_cache, block_table, lengths, kv_scale, what):
+    """(fp8, num_pages, page_size, Hkv, d) of a paged cache's checked tensors."""
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must be [num_pages, page_size, Hkv, d]")
+    fp8 = k_cache.dtype in _CODES
+    if not fp8 and k_cache.dtype != torch.bfloat16 or v_cache.dtype != k_cache.dtype:
+        raise TypeError("k_cache and v_cache must both be bfloat16, or float8_e4m3fn (or its uint8 codes)")
+    num_pages, page_size, Hkv, d = k_cache.shape
+    tensors = [v_cache, block_table, lengths]
+    if fp8:
+        if kv_scale is None:
+            raise ValueError("an 8-bit cache needs kv_scale [num_pages, Hkv, 2, page_size]")
+        if kv_scale.dtype not in _SCALES:
+            raise TypeError("kv_scale must be uint8 (or float8_e8m0fnu)")
+        if kv_scale.shape != (num_pages, Hkv, 2, page_size):
+            raise ValueError("kv_scale must be [num_pages, Hkv, 2, page_size]")
+        tensors.append(kv_scale)
+    elif kv_scale is not None:
+        raise ValueError("a bfloat16 cache takes no kv_scale")
+    if block_table.dtype != torch.int32 or lengths.dtype != torch.int32:
+        raise TypeError(f"block_table and {what} must be int32")
+    if block_table.dim() != 2 or lengths.shape != block_table.shape[:1]:
+        raise ValueError(f"block_table must be [B, max_pages] and {what} [B]")
+    if not k_cache.is_contiguous():
+        raise ValueError("cache tensors must be contiguous")
+    for t in tensors:
+        if not t.is_contiguous():
+            raise ValueError("cache tensors must be contiguous")
+        if t.device != k_cache.device:
+            raise ValueError("all tensors must share one device")
+    if not k_cache.is_cuda:
+        raise ValueError("tensors must live on a CUDA device (there is no CPU path)")
+    return fp8, num_pages, page_size, Hkv, d
+
+
+def cache_append(k, v, k_cache, v_cache, block_table, start, kv_scale=None, count=None, stream=None):
+    """Write new tokens' K and V rows into a paged cache, in place (fa_cache_append).
+
+    k, v: [B, N, Hkv, d] bf16 (strided views too); row n of sequence b becomes its
+    position start[b] + n.  k_cache, v_cache: [num_pages, page_size, Hkv, d], bf16, or
+    float8_e4m3fn (or uint8 codes) with kv_scale [num_pages, Hkv, 2, page_size] uint8
+    (or float8_e8m0fnu), a power-of-two scale per row.  block_table [B, max_pages],
+    start [B] and the optional count [B] (rows of each sequence, None: N) are int32.
+    """
+    fp8, num_pages, page_size, Hkv, d = _cache_check(k_cache, v_cache, block_table, start, kv_scale, "start")
+    if k.dim() != 4 or v.shape != k.shape or k.shape[0] != block_table.shape[0] or k.shape[2:] != (Hkv, d):
+        raise ValueError("k and v must be [B, N, Hkv, d] for the cache's Hkv and d and block_table's B")
+    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
+        raise TypeError("k and v must be bfloat16")
+    if k.device != k_cache.device or v.device != k_cache.device:
+        raise ValueError("all tensors must share one device")
+    if count is not None:
+        if count.dtype != torch.int32:
+            raise TypeError("count must be int32")
+        if count.shape != start.shape or not count.is_contiguous() or count.device != k_cache.device:
+            raise ValueError("count must be a contiguous [B] tensor on the cache's device")
+    ks, vs = _strides(k, "k"), _strides(v, "v")
+
+    def call(handle):
+        rc = lib().fa_cache_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(kv_scale),
+                                   block_table.data_ptr(), start.data_ptr(), _ptr(count), k.shape[0], k.shape[1], Hkv,
+                                   d, ks, vs, page_size, num_pages, block_table.shape[1], 1 if fp8 else 0, handle)
+        if rc != 0:
+            raise FAError(rc, "fa_cache_append")
+
+    _launch(k_cache.device, stream, call)
+
+
+def cache_read(k_cache, v_cache, block_table, seqlens, length: int, kv_scale=None, k_out=None, v_out=None,
+               stream=None):
+    """The first ``length`` positions of every sequence out of a paged cache (fa_cache_read): returns
+    (k, v) [B, length, Hkv, d] bf16, zeros at and past seqlens[b].  Cache tensors as in ``cache_append``."""
+    fp8, num_pages, page_size, Hkv, d = _cache_check(k_cache, v_cache, block_table, seqlens, kv_scale, "seqlens")
+    B, N = block_table.shape[0], int(length)
+
+    def call(handle):
+        k = _out_like(k_out, (B, N, Hkv, d), torch.bfloat16, k_cache.device, "k_out")
+        v = _out_like(v_out, (B, N, Hkv, d), torch.bfloat16, k_cache.device, "v_out")
+        rc = lib().fa_cache_read(k_cache.data_ptr(), v_cache.data_ptr(), _ptr(kv_scale), block_table.data_ptr(),
+                                 seqlens.data_ptr(), k.data_ptr(), v.data_ptr(), B, N, Hkv, d, page_size, num_pages,
+                                 block_table.shape[1], 1 if fp8 else 0, handle)
+        if rc != 0:
+            raise FAError(rc, "fa_cache_read")
+        return k, v
+
+    return _launch(k_cache.device, stream, call)
+
+
+def decode_fp8_workspace_size(B: int, H: int, Hkv: int, d: int, page_size: int, max_pages: int,
+                              window_left: int | None = None) -> int:
+    """Workspace bytes with which ``decode_paged_fp8`` splits long sequences as it would unconstrained."""
+    return int(lib().fa_decode_fp8_workspace_size(B, H, Hkv, d, page_size, max_pages,
+                                                  -1 if window_left is None else int(window_left)))
+
+
+def decode_paged_fp8(q, k_cache, v_cache, kv_scale, block_table, seqlens, scale: float | None = None,
+                     window_left: int | None = None, out=None, lse=None, workspace=None, stream=None):
+    """One decode step over a paged 8-bit cache (fa_decode_paged_fp8): returns (o [B, H, d] bf16, lse [B, H] fp32).
+
+    q: [B, H, d] bf16; the cache as ``cache_append`` writes it.  ``window_left``:
+    the query sees its own position (the sequence's last) and that many before it.
+    ``workspace`` (uint8 cuda tensor) defaults to a fresh buffer of
+    ``decode_fp8_workspace_size`` bytes.
+    """
+    if k_cache.dtype not in _CODES:
+        raise TypeError("decode_paged_fp8 takes an 8-bit cache (decode_paged: bfloat16)")
+    _, num_pages, page_size, Hkv, d = _cache_check(k_cache, v_cache, block_table, seqlens, kv_scale, "seqlens")
+    if q.dim() != 3 or q.shape[0] != block_table.shape[0] or q.shape[2] != d:
+        raise ValueError("q must be [B, H, d] for block_table's B and the cache's d")
+    if q.dtype != torch.bfloat16:
+        raise TypeError("q must be bfloat16")
+    if q.device != k_cache.device or not q.is_contiguous():
+        raise ValueError("q must be contiguous, on the cache's device")
+    if window_left is not None and (int(window_left) != window_left or window_left < 0):
+        raise ValueError("window_left must be None or an integer >= 0")
+    if workspace is not None and (workspace.device != q.device or not workspace.is_contiguous()):
+        raise ValueError("workspace must be contiguous, on the device of q")
+    B, H = q.shape[0], q.shape[1]
+    max_pages = block_table.shape[1]
+    w = -1 if window_left is None else min(int(window_left), 1 << 30)
+
+    def call(handle):
+        o = _out_like(out, (B, H, d), torch.bfloat16, q.device, "out")
+        l = _out_like(lse, (B, H), torch.float32, q.device, "lse")
+        ws, size = workspace, 0
+        if ws is None:
+            size = lib().fa_decode_fp8_workspace_size(B, H, Hkv, d, page_size, max_pages, w)
+            if size:
+                ws = torch.empty(size, dtype=torch.uint8, device=q.device)
+        else:
+            size = ws.numel() * ws.element_size()
+        rc = lib().fa_decode_paged_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kv_scale.data_ptr(),
+                                       block_table.data_ptr(), seqlens.data_ptr(), o.data_ptr(), l.data_ptr(), B, H,
+                                       Hkv, d, page_size, num_pages, max_pages, _scale(scale, d), w, _ptr(ws), size,
+                                       handle)
+        if rc != 0:
+            raise FAError(rc, "fa_decode_paged_fp8")
+        return o, l
+
+    return _launch(q.device, stream, call)

@@ -27,7 +27,7 @@ BUILD = PKG / "_build"
 LIB = PKG / "libfa.so"
 SOURCES = ("fa_api.cu", "fa_fwd_bf16.cu", "fa_fwd_fp8.cu", "fa_fwd_f32.cu", "fa_bwd.cu",
            "fa_bwd_static.cu", "fa_ring.cu",
-           "fa_bwd64.cu", "fa_decode.cu")
+           "fa_bwd64.cu", "fa_decode.cu", "fa_rope.cu", "fa_cache.cu", "fa_decode_fp8.cu")
 PROBE_SOURCES = ("fa_probe.cu",)
 PROBE_LIB = PKG / "libfa_probe.so"
 DEBUG_LIB = PKG / "libfa_debug.so"

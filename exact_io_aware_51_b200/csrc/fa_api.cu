@@ -244,6 +244,18 @@ CUresult make_paged_map(CUtensorMap* map, const void* base, int num_pages, int p
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
+CUresult make_paged_map_u8(CUtensorMap* map, const void* base, int num_pages, int page_size, int Hkv, int d) {
+  if (!encoder()) return CUDA_ERROR_NOT_FOUND;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(Hkv) * d,
+                              static_cast<cuuint64_t>(num_pages) * static_cast<cuuint64_t>(page_size)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(Hkv) * d};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(page_size < 128 ? page_size : 128)};
+  const cuuint32_t estr[2] = {1u, 1u};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
 CUresult make_tile_map_e4m3(CUtensorMap* map, const void* base, int B, int N, int H, int d, int rows) {
   if (!encoder()) return CUDA_ERROR_NOT_FOUND;
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(H),
@@ -804,6 +816,361 @@ int fa_decode_paged(const void* Q, const void* K_cache, const void* V_cache, con
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (t_ev_start) cudaEventRecord(t_ev_start, s);
   cudaError_t e = launch_decode(tk, tv, a, make_ctl(*st), s);
+  if (t_ev_stop && e == cudaSuccess) cudaEventRecord(t_ev_stop, s);
+  if (e != cudaSuccess) return fail_cuda(e);
+  return FA_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Norm and rotation of query and key heads
+// ---------------------------------------------------------------------------
+namespace {
+
+// Warps per launch that keep every SM's warp slots filled about twice over; below
+// that a warp takes fewer row groups of its position.
+constexpr long long kFullWarps = 148LL * 64;
+constexpr int kRopeBlockWarps = 4;
+constexpr int kRopeBwdBlocks = 148 * 6;
+
+bool aligned_strides(const long long* s, int dtype) {
+  const long long m = dtype == FA_BF16 ? 8 : 4;  // 16 bytes
+  return s == nullptr || (s[0] % m == 0 && s[1] % m == 0 && s[2] % m == 0);
+}
+
+void set_strides(const long long* s, int N, int heads, int d, long long* sb, long long* sn, long long* sh) {
+  *sh = s ? s[2] : d;
+  *sn = s ? s[1] : static_cast<long long>(heads) * d;
+  *sb = s ? s[0] : static_cast<long long>(N) * heads * d;
+}
+
+int check_rope(const void* Q, const void* K, const void* wq, const void* wk, const float* cos_t, const float* sin_t,
+               const void* Qo, const void* Ko, const int* positions, int B, int N, int H, int Hkv, int d,
+               int table_rows, float eps, int interleaved, int dtype, int weight_dtype) {
+  int rc = check_shape(B, H, N, d, dtype);
+  if (rc) return rc;
+  if (Hkv < 0 || table_rows < 0) return FA_ERR_INVALID_ARG;
+  if (Hkv > 65535 || static_cast<long long>(B) * N > 0x7fffffffLL) return FA_ERR_TOO_LARGE;
+  if ((interleaved != 0 && interleaved != 1) || (weight_dtype != FA_BF16 && weight_dtype != FA_FP32))
+    return FA_ERR_INVALID_ARG;
+  if (!std::isfinite(eps) || eps < 0.f) return FA_ERR_INVALID_ARG;
+  if ((wq == nullptr) != (wk == nullptr)) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(B) * N == 0 || H + Hkv == 0) return FA_OK;
+  if (!positions && N > table_rows) return FA_ERR_INVALID_ARG;
+  if ((H > 0 && (!Q || !Qo)) || (Hkv > 0 && (!K || !Ko)) || !cos_t || !sin_t) return FA_ERR_INVALID_ARG;
+  if (!aligned16(Q) || !aligned16(K) || !aligned16(Qo) || !aligned16(Ko) || !aligned16(wq) || !aligned16(wk) ||
+      !aligned16(cos_t) || !aligned16(sin_t) || (reinterpret_cast<uintptr_t>(positions) & 3u))
+    return FA_ERR_MISALIGNED;
+  return FA_OK;
+}
+
+RopeArgs rope_args(const void* Q, const void* K, const void* wq, const void* wk, const float* cos_t, const float* sin_t,
+                   const int* positions, void* Qo, void* Ko, int B, int N, int H, int Hkv, int d,
+                   const long long* qs, const long long* ks, int table_rows, float eps, int interleaved,
+                   int weight_dtype, int* status) {
+  RopeArgs a = {};
+  a.q.x = Q;
+  a.k.x = K;
+  set_strides(qs, N, H, d, &a.q.sb, &a.q.sn, &a.q.sh);
+  set_strides(ks, N, Hkv, d, &a.k.sb, &a.k.sn, &a.k.sh);
+  a.q.out = Qo;
+  a.k.out = Ko;
+  a.q.w = wq;
+  a.k.w = wk;
+  a.cos_t = cos_t;
+  a.sin_t = sin_t;
+  a.positions = positions;
+  a.tokens = B * N;
+  a.N = N;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.table = table_rows;
+  a.interleaved = interleaved;
+  a.w_f32 = weight_dtype == FA_FP32;
+  a.eps = eps;
+  a.status = status;
+  const int rows = 512 / d;
+  const long long groups = (H + rows - 1) / rows + (Hkv + rows - 1) / rows;
+  a.per = 8;
+  while (a.per > 1 && a.tokens * ((groups + a.per - 1) / a.per) < kFullWarps) a.per /= 2;
+  a.q_groups = (H + rows * a.per - 1) / (rows * a.per);
+  a.k_groups = (Hkv + rows * a.per - 1) / (rows * a.per);
+  return a;
+}
+
+// Blocks of the backward: as many as fill the GPU, shared between q and k by their heads.
+void rope_blocks(RopeArgs* a) {
+  const long long qu = static_cast<long long>(a->tokens) * a->q_groups, ku = static_cast<long long>(a->tokens) * a->k_groups;
+  const long long qw = (qu + kRopeBlockWarps - 1) / kRopeBlockWarps, kw = (ku + kRopeBlockWarps - 1) / kRopeBlockWarps;
+  if (qw + kw <= kRopeBwdBlocks) {
+    a->q_blocks = static_cast<int>(qw);
+    a->blocks = static_cast<int>(qw + kw);
+    return;
+  }
+  const long long want = static_cast<long long>(kRopeBwdBlocks) * a->H / (a->H + a->Hkv);
+  a->q_blocks = static_cast<int>(std::min(qw, std::max<long long>(a->H ? 1 : 0, std::min<long long>(want, kRopeBwdBlocks - (a->Hkv ? 1 : 0)))));
+  a->blocks = a->q_blocks + static_cast<int>(std::min(kw, static_cast<long long>(kRopeBwdBlocks - a->q_blocks)));
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_qk_norm_rope(const void* Q, const void* K, const void* q_weight, const void* k_weight, const float* cos_table,
+                    const float* sin_table, const int* positions, void* Q_out, void* K_out, int B, int N, int H,
+                    int Hkv, int d, const long long* q_strides, const long long* k_strides, int table_rows, float eps,
+                    int interleaved, int dtype, int weight_dtype, void* stream) {
+  int rc = check_rope(Q, K, q_weight, k_weight, cos_table, sin_table, Q_out, K_out, positions, B, N, H, Hkv, d,
+                      table_rows, eps, interleaved, dtype, weight_dtype);
+  if (rc) return rc;
+  if (static_cast<long long>(B) * N == 0 || H + Hkv == 0) return FA_OK;
+  if (!aligned_strides(q_strides, dtype) || !aligned_strides(k_strides, dtype)) return FA_ERR_MISALIGNED;
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st))) return rc;
+  const RopeArgs a = rope_args(Q, K, q_weight, k_weight, cos_table, sin_table, positions, Q_out, K_out, B, N, H, Hkv, d,
+                               q_strides, k_strides, table_rows, eps, interleaved, weight_dtype, st->status);
+  const cudaError_t e = launch_rope_fwd(a, d, dtype == FA_FP32, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : fail_cuda(e);
+}
+
+size_t fa_qk_norm_rope_workspace_size(int d) {
+  if (d != 64 && d != 128) return 0;
+  return align256(static_cast<size_t>(kRopeBwdBlocks) * d * sizeof(float));
+}
+
+int fa_qk_norm_rope_bwd(const void* Q, const void* K, const void* q_weight, const void* k_weight,
+                        const float* cos_table, const float* sin_table, const int* positions, const void* dQ_out,
+                        const void* dK_out, void* dQ, void* dK, void* dq_weight, void* dk_weight, int B, int N, int H,
+                        int Hkv, int d, const long long* q_strides, const long long* k_strides,
+                        const long long* dq_out_strides, const long long* dk_out_strides, int table_rows, float eps,
+                        int interleaved, int dtype, int weight_dtype, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+  int rc = check_rope(Q, K, q_weight, k_weight, cos_table, sin_table, dQ, dK, positions, B, N, H, Hkv, d, table_rows,
+                      eps, interleaved, dtype, weight_dtype);
+  if (rc) return rc;
+  const bool norm = q_weight != nullptr;
+  const bool empty = static_cast<long long>(B) * N == 0 || H + Hkv == 0;
+  if (!norm && empty) return FA_OK;
+  if (norm && (!dq_weight || !dk_weight)) return FA_ERR_INVALID_ARG;
+  if (!empty && ((H > 0 && !dQ_out) || (Hkv > 0 && !dK_out))) return FA_ERR_INVALID_ARG;
+  if (!aligned16(dQ_out) || !aligned16(dK_out) || !aligned16(dq_weight) || !aligned16(dk_weight) ||
+      !aligned_strides(q_strides, dtype) || !aligned_strides(k_strides, dtype) ||
+      !aligned_strides(dq_out_strides, dtype) || !aligned_strides(dk_out_strides, dtype))
+    return FA_ERR_MISALIGNED;
+  if (norm && (!workspace || workspace_bytes < fa_qk_norm_rope_workspace_size(d) ||
+               (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+    return FA_ERR_WORKSPACE;
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st))) return rc;
+  RopeArgs a = rope_args(Q, K, q_weight, k_weight, cos_table, sin_table, positions, dQ, dK, B, N, H, Hkv, d, q_strides,
+                         k_strides, table_rows, eps, interleaved, weight_dtype, st->status);
+  a.q.g = dQ_out;
+  a.k.g = dK_out;
+  set_strides(dq_out_strides, N, H, d, &a.q.gb, &a.q.gn, &a.q.gh);
+  set_strides(dk_out_strides, N, Hkv, d, &a.k.gb, &a.k.gn, &a.k.gh);
+  if (!empty) rope_blocks(&a);
+  a.partial = static_cast<float*>(workspace);
+  a.dwq = dq_weight;
+  a.dwk = dk_weight;
+  const cudaError_t e = launch_rope_bwd(a, d, dtype == FA_FP32, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : fail_cuda(e);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Paged cache: writing new tokens, reading cached positions, 8-bit decode
+// ---------------------------------------------------------------------------
+namespace {
+
+int check_cache(const void* K_cache, const void* V_cache, const void* kv_scale, const int* block_table,
+                const int* lengths, int B, int N, int Hkv, int d, int page_size, int num_pages, int max_pages,
+                int fp8) {
+  if (B < 0 || N < 0 || Hkv < 1 || num_pages < 1 || max_pages < 1 || (fp8 != 0 && fp8 != 1)) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+  if (!pow2_in(page_size, 8, 4096)) return FA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(num_pages) * page_size > 0x7fffffffLL ||
+      static_cast<long long>(max_pages) * page_size > (1LL << 30) || B > 65535 || Hkv > 65535)
+    return FA_ERR_TOO_LARGE;
+  // one warp per (sequence, 512 / d positions, head)
+  const long long groups = (static_cast<long long>(N) * d + 511) / 512;
+  if (static_cast<double>(B) * groups * Hkv >= 4294967296.0) return FA_ERR_TOO_LARGE;
+  if (B == 0 || N == 0) return FA_OK;
+  if (!K_cache || !V_cache || !block_table || !lengths || (fp8 && !kv_scale)) return FA_ERR_INVALID_ARG;
+  if (!aligned16(K_cache) || !aligned16(V_cache) || (fp8 && !aligned16(kv_scale)) ||
+      (reinterpret_cast<uintptr_t>(block_table) & 3u) || (reinterpret_cast<uintptr_t>(lengths) & 3u))
+    return FA_ERR_MISALIGNED;
+  return FA_OK;
+}
+
+CacheArgs cache_args(void* K_cache, void* V_cache, void* kv_scale, const int* block_table, const int* lengths, int B,
+                     int N, int Hkv, int d, int page_size, int num_pages, int max_pages, int* status) {
+  CacheArgs a = {};
+  a.t[0].pool = K_cache;
+  a.t[1].pool = V_cache;
+  a.kv_scale = static_cast<uint8_t*>(kv_scale);
+  a.block_table = block_table;
+  a.start = lengths;
+  a.N = N;
+  a.Hkv = Hkv;
+  a.page_size = page_size;
+  while ((1 << a.page_shift) < page_size) ++a.page_shift;
+  a.num_pages = num_pages;
+  a.max_pages = max_pages;
+  a.groups = static_cast<unsigned int>((static_cast<long long>(N) * d + 511) / 512);
+  a.units = static_cast<unsigned int>(B) * a.groups * static_cast<unsigned int>(Hkv);
+  a.status = status;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_cache_append(const void* K, const void* V, void* K_cache, void* V_cache, void* kv_scale, const int* block_table,
+                    const int* start, const int* count, int B, int N, int Hkv, int d, const long long* k_strides,
+                    const long long* v_strides, int page_size, int num_pages, int max_pages, int fp8, void* stream) {
+  int rc = check_cache(K_cache, V_cache, kv_scale, block_table, start, B, N, Hkv, d, page_size, num_pages, max_pages, fp8);
+  if (rc) return rc;
+  if (B == 0 || N == 0) return FA_OK;
+  if (!K || !V) return FA_ERR_INVALID_ARG;
+  if (!aligned16(K) || !aligned16(V) || !aligned_strides(k_strides, FA_BF16) || !aligned_strides(v_strides, FA_BF16) ||
+      (reinterpret_cast<uintptr_t>(count) & 3u))
+    return FA_ERR_MISALIGNED;
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st))) return rc;
+  CacheArgs a = cache_args(K_cache, V_cache, kv_scale, block_table, start, B, N, Hkv, d, page_size, num_pages,
+                           max_pages, st->status);
+  a.t[0].x = K;
+  a.t[1].x = V;
+  set_strides(k_strides, N, Hkv, d, &a.t[0].sb, &a.t[0].sn, &a.t[0].sh);
+  set_strides(v_strides, N, Hkv, d, &a.t[1].sb, &a.t[1].sn, &a.t[1].sh);
+  a.count = count;
+  const cudaError_t e = launch_cache(a, d, fp8 != 0, true, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : fail_cuda(e);
+}
+
+int fa_cache_read(const void* K_cache, const void* V_cache, const void* kv_scale, const int* block_table,
+                  const int* seqlens, void* K, void* V, int B, int N, int Hkv, int d, int page_size, int num_pages,
+                  int max_pages, int fp8, void* stream) {
+  int rc = check_cache(K_cache, V_cache, kv_scale, block_table, seqlens, B, N, Hkv, d, page_size, num_pages, max_pages,
+                       fp8);
+  if (rc) return rc;
+  if (B == 0 || N == 0) return FA_OK;
+  if (!K || !V) return FA_ERR_INVALID_ARG;
+  if (!aligned16(K) || !aligned16(V)) return FA_ERR_MISALIGNED;
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st))) return rc;
+  CacheArgs a = cache_args(const_cast<void*>(K_cache), const_cast<void*>(V_cache), const_cast<void*>(kv_scale),
+                           block_table, seqlens, B, N, Hkv, d, page_size, num_pages, max_pages, st->status);
+  a.t[0].out = K;
+  a.t[1].out = V;
+  const cudaError_t e = launch_cache(a, d, fp8 != 0, false, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : fail_cuda(e);
+}
+
+}  // extern "C"
+
+namespace {
+
+struct Decode8Plan {
+  int nt, hgroups, splits, chunk;
+  size_t ws;
+};
+
+int check_decode8(int B, int H, int Hkv, int d, int page_size, int num_pages, int max_pages, float scale, int window) {
+  int rc = check_decode(B, H, Hkv, d, page_size, num_pages, max_pages, scale);
+  if (rc) return rc;
+  if (window < -1) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(max_pages) * page_size > (1LL << 30)) return FA_ERR_TOO_LARGE;
+  if (static_cast<long long>(B) * H > 0x7fffffffLL) return FA_ERR_TOO_LARGE;
+  return FA_OK;
+}
+
+// Chunks of positions per (sequence, head group), in tiles of 128.
+Decode8Plan decode8_plan(int B, int H, int Hkv, int d, int page_size, int max_pages, int window, size_t ws_cap) {
+  Decode8Plan p;
+  const int G = H / Hkv;
+  p.nt = G <= 8 ? 1 : 2;
+  p.hgroups = (G + 8 * p.nt - 1) / (8 * p.nt);
+  long long span = static_cast<long long>(max_pages) * page_size;
+  // a window's first position lies anywhere in its first tile
+  if (window >= 0) span = std::min(span, static_cast<long long>(window) + 1 + 127);
+  const long long tiles = (span + 127) / 128;
+  const long long ctas = static_cast<long long>(B) * Hkv * p.hgroups;
+  const long long slots = 2 * 148;
+  const long long min_tiles = d == 128 ? 8 : 16;
+  const long long w = ctas < slots ? 2 : 4;
+  long long want = ctas <= 0 ? 1 : (w * slots + ctas - 1) / ctas;
+  want = std::max(1LL, std::min({want, tiles / min_tiles, 65535LL}));
+  for (;;) {
+    const long long chunk_tiles = (tiles + want - 1) / want;
+    p.splits = static_cast<int>((tiles + chunk_tiles - 1) / chunk_tiles);
+    p.chunk = static_cast<int>(chunk_tiles * 128);
+    p.ws = decode_ws_bytes(B, H, d, p.splits);
+    if (p.splits == 1 || p.ws <= ws_cap) break;
+    want = p.splits - 1;
+  }
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fa_decode_fp8_workspace_size(int B, int H, int Hkv, int d, int page_size, int max_pages, int window_left) {
+  if (check_decode8(B, H, Hkv, d, page_size, 1, max_pages, 1.0f, window_left) != FA_OK) return 0;
+  return decode8_plan(B, H, Hkv, d, page_size, max_pages, window_left, SIZE_MAX).ws;
+}
+
+int fa_decode_paged_fp8(const void* Q, const void* K_cache, const void* V_cache, const void* kv_scale,
+                        const int* block_table, const int* seqlens, void* O, float* LSE, int B, int H, int Hkv, int d,
+                        int page_size, int num_pages, int max_pages, float scale, int window_left, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  int rc = check_decode8(B, H, Hkv, d, page_size, num_pages, max_pages, scale, window_left);
+  if (rc) return rc;
+  if (B == 0) return FA_OK;
+  if (!Q || !K_cache || !V_cache || !kv_scale || !block_table || !seqlens || !O || !LSE) return FA_ERR_INVALID_ARG;
+  if (!aligned16(Q) || !aligned16(K_cache) || !aligned16(V_cache) || !aligned16(kv_scale) || !aligned16(O) ||
+      (reinterpret_cast<uintptr_t>(LSE) & 3u) || (reinterpret_cast<uintptr_t>(block_table) & 3u) ||
+      (reinterpret_cast<uintptr_t>(seqlens) & 3u))
+    return FA_ERR_MISALIGNED;
+  if (workspace && !aligned16(workspace)) return FA_ERR_WORKSPACE;
+  DeviceState* st = nullptr;
+  if ((rc = device_state(&st))) return rc;
+  const Decode8Plan plan =
+      decode8_plan(B, H, Hkv, d, page_size, max_pages, window_left, workspace ? workspace_bytes : 0);
+  Decode8Args a = {};
+  a.B = B;
+  a.H = H;
+  a.Hkv = Hkv;
+  a.page_size = page_size;
+  a.num_pages = num_pages;
+  a.max_pages = max_pages;
+  a.hgroups = plan.hgroups;
+  a.splits = plan.splits;
+  a.chunk = plan.chunk;
+  a.window = window_left;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.Q = Q;
+  a.kv_scale = static_cast<const uint8_t*>(kv_scale);
+  a.block_table = block_table;
+  a.seqlens = seqlens;
+  a.O = O;
+  a.LSE = LSE;
+  const size_t rows = static_cast<size_t>(plan.splits) * B * H;
+  a.Opart = plan.splits > 1 ? static_cast<float*>(workspace) : nullptr;
+  a.LSEpart = plan.splits > 1 ? reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(rows * d * 4))
+                              : nullptr;
+  CUtensorMap tk, tv;
+  CUresult r;
+  if ((r = make_paged_map_u8(&tk, K_cache, num_pages, page_size, Hkv, d)) != CUDA_SUCCESS ||
+      (r = make_paged_map_u8(&tv, V_cache, num_pages, page_size, Hkv, d)) != CUDA_SUCCESS)
+    return fail_encode(r);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (t_ev_start) cudaEventRecord(t_ev_start, s);
+  cudaError_t e = launch_decode_fp8(tk, tv, a, d, plan.nt, make_ctl(*st), s);
   if (t_ev_stop && e == cudaSuccess) cudaEventRecord(t_ev_stop, s);
   if (e != cudaSuccess) return fail_cuda(e);
   return FA_OK;

@@ -132,6 +132,82 @@ CUresult make_paged_map(CUtensorMap* map, const void* base, int num_pages, int p
 cudaError_t launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeArgs& a, const DevCtl& c,
                           cudaStream_t s);
 
+// One decode step over a paged 8-bit KV cache: e4m3 pools [num_pages, page_size, Hkv, d],
+// scale bytes [num_pages, Hkv, 2, page_size] (K's, then V's; the value is 2^(byte - 127)).
+struct Decode8Args {
+  int B, H, Hkv;
+  int page_size, num_pages, max_pages;
+  int hgroups;       // CTAs per K/V head: groups of at most 8 * nt query heads
+  int splits;        // chunks of positions per (sequence, head group)
+  int chunk;         // positions per chunk (a multiple of 128)
+  int window;        // the query's own position and `window` before it are visible; -1: all
+  float scale_log2;  // softmax scale * log2(e)
+  const void* Q;
+  const uint8_t* kv_scale;
+  const int* block_table;
+  const int* seqlens;
+  void* O;           // [B, H, d] bf16
+  float* LSE;        // [B, H] natural log
+  float* Opart;      // splits > 1: [splits, B, H, d] fp32, normalised per chunk
+  float* LSEpart;    // splits > 1: [splits, B, H] natural log (-inf: no position; +inf: not to be used)
+};
+
+// TMA descriptor for an 8-bit paged pool viewed as [num_pages * page_size rows][Hkv * d
+// bytes]: a box of min(page_size, 128) rows x d bytes, swizzled over its d bytes.
+CUresult make_paged_map_u8(CUtensorMap* map, const void* base, int num_pages, int page_size, int Hkv, int d);
+// nt: 8-head column blocks per CTA (1 or 2)
+cudaError_t launch_decode_fp8(const CUtensorMap& tk, const CUtensorMap& tv, const Decode8Args& a, int d, int nt,
+                              const DevCtl& c, cudaStream_t s);
+
+// Norm and rotation of query and key heads.  Strides count elements.
+struct RopeTensor {
+  const void* x;         // [B, N, heads, d], features contiguous
+  long long sb, sn, sh;  // strides of x: batch, position, head
+  const void* g;         // backward: the gradient of the output, as x
+  long long gb, gn, gh;
+  void* out;             // dense [B, N, heads, d]: the output (forward), the gradient of x (backward)
+  const void* w;         // gain [d] (nullptr: no norm)
+};
+struct RopeArgs {
+  RopeTensor q, k;
+  const float* cos_t;    // [table, d / 2]
+  const float* sin_t;
+  const int* positions;  // [B, N] or nullptr: 0 .. N - 1
+  int tokens, N;         // tokens = B * N
+  int H, Hkv, table;
+  int per;               // row groups (of 512 / d heads) a warp takes at one position
+  int q_groups, k_groups;  // warps per position for q and k
+  int interleaved, w_f32;
+  float eps;
+  int* status;
+  // backward
+  int q_blocks, blocks;  // blocks of q, and of both
+  float* partial;        // [blocks, d] fp32 sums of the gains' gradients
+  void* dwq;
+  void* dwk;
+};
+cudaError_t launch_rope_fwd(const RopeArgs& a, int d, bool f32, cudaStream_t s);
+cudaError_t launch_rope_bwd(const RopeArgs& a, int d, bool f32, cudaStream_t s);
+
+// Paged cache writes and reads.  Strides count elements.
+struct CacheTensor {
+  const void* x;         // append: new rows [B, N, Hkv, d] bf16, features contiguous
+  long long sb, sn, sh;
+  void* pool;            // [num_pages, page_size, Hkv, d]
+  void* out;             // read: dense [B, N, Hkv, d] bf16
+};
+struct CacheArgs {
+  CacheTensor t[2];      // K, V
+  uint8_t* kv_scale;     // [num_pages, Hkv, 2, page_size], 8-bit pools only
+  const int* block_table;
+  const int* start;      // [B] append: the position of the first new row; read: seqlens
+  const int* count;      // [B] append: new rows of each sequence, nullptr: N
+  int N, Hkv, page_size, page_shift, num_pages, max_pages;
+  unsigned int units, groups;  // warps; groups of 512 / d positions per sequence
+  int* status;
+};
+cudaError_t launch_cache(const CacheArgs& a, int d, bool fp8, bool append, cudaStream_t s);
+
 // Kernel launchers (each returns the cudaError_t of the launch).
 cudaError_t launch_fwd_bf16(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                             const CUtensorMap& to, const FwdArgs& a, const DevCtl& c, cudaStream_t s);

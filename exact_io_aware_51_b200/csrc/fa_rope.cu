@@ -1,0 +1,449 @@
+// RMS norm of query and key heads with the rotation by position, in one pass,
+// and its backward; bf16 and fp32, d = 64 or 128, sm_100a.
+//
+// For one row x (d features of one head at one position) with gain w:
+//     r = 1 / sqrt(mean(x^2) + eps),   y = x r w
+// and, for every pair (first, second) of features with the position's angle
+// (c, s) from the caller's tables,
+//     out_first = y_first c - y_second s,   out_second = y_second c + y_first s.
+// Pairs are (i, i + d/2), or (2i, 2i + 1) when interleaved.  The rotation is
+// orthogonal, so with the incoming gradient g and gr = R^T g
+//     dw = sum over rows of gr x r,
+//     dx = r w gr - x r^3 / d * sum(w gr x).
+// The backward recomputes r from x (which it has to read anyway), so the
+// forward saves nothing.
+//
+// Both are bound by the bytes they move (x in, out; x, g in, dx out).  A lane
+// holds 16 features of a row: 8 from each half, so both elements of a pair are
+// in one thread in either layout, the loads and stores are 16 bytes wide, and
+// a row takes d / 16 lanes (a warp 4 rows of d = 128, 8 of d = 64).  A warp
+// takes the heads of one position, so the angles and gains are read once for
+// all of them.  All arithmetic is fp32 (packed pairs), each output is rounded
+// once.
+#include <cuda_bf16.h>
+
+#include "fa_internal.h"
+#include "sm100.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kWarps = 4;
+
+// 16 features of one row: two runs of 8 (first half, second half)
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  uint4 a, b;
+};
+template <>
+struct Raw<float> {
+  float4 a0, a1, b0, b1;
+};
+
+template <int D>
+__device__ __forceinline__ void load_row(Raw<__nv_bfloat16>& r, const __nv_bfloat16* p, int sub) {
+  r.a = *reinterpret_cast<const uint4*>(p + 8 * sub);
+  r.b = *reinterpret_cast<const uint4*>(p + D / 2 + 8 * sub);
+}
+template <int D>
+__device__ __forceinline__ void load_row(Raw<float>& r, const float* p, int sub) {
+  r.a0 = *reinterpret_cast<const float4*>(p + 8 * sub);
+  r.a1 = *reinterpret_cast<const float4*>(p + 8 * sub + 4);
+  r.b0 = *reinterpret_cast<const float4*>(p + D / 2 + 8 * sub);
+  r.b1 = *reinterpret_cast<const float4*>(p + D / 2 + 8 * sub + 4);
+}
+
+__device__ __forceinline__ float2 bf2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+
+// x[0..3]: the run of the first half as pairs of neighbours, x[4..7]: of the second
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16>& r, float2 (&x)[8]) {
+  x[0] = bf2(r.a.x);
+  x[1] = bf2(r.a.y);
+  x[2] = bf2(r.a.z);
+  x[3] = bf2(r.a.w);
+  x[4] = bf2(r.b.x);
+  x[5] = bf2(r.b.y);
+  x[6] = bf2(r.b.z);
+  x[7] = bf2(r.b.w);
+}
+__device__ __forceinline__ void unpack(const Raw<float>& r, float2 (&x)[8]) {
+  x[0] = make_float2(r.a0.x, r.a0.y);
+  x[1] = make_float2(r.a0.z, r.a0.w);
+  x[2] = make_float2(r.a1.x, r.a1.y);
+  x[3] = make_float2(r.a1.z, r.a1.w);
+  x[4] = make_float2(r.b0.x, r.b0.y);
+  x[5] = make_float2(r.b0.z, r.b0.w);
+  x[6] = make_float2(r.b1.x, r.b1.y);
+  x[7] = make_float2(r.b1.z, r.b1.w);
+}
+
+template <int D>
+__device__ __forceinline__ void store_row(__nv_bfloat16* p, int sub, const float2 (&x)[8]) {
+  uint4 a, b;
+  a.x = pack_bf16x2(x[0].x, x[0].y);
+  a.y = pack_bf16x2(x[1].x, x[1].y);
+  a.z = pack_bf16x2(x[2].x, x[2].y);
+  a.w = pack_bf16x2(x[3].x, x[3].y);
+  b.x = pack_bf16x2(x[4].x, x[4].y);
+  b.y = pack_bf16x2(x[5].x, x[5].y);
+  b.z = pack_bf16x2(x[6].x, x[6].y);
+  b.w = pack_bf16x2(x[7].x, x[7].y);
+  *reinterpret_cast<uint4*>(p + 8 * sub) = a;
+  *reinterpret_cast<uint4*>(p + D / 2 + 8 * sub) = b;
+}
+template <int D>
+__device__ __forceinline__ void store_row(float* p, int sub, const float2 (&x)[8]) {
+  float4* a = reinterpret_cast<float4*>(p + 8 * sub);
+  float4* b = reinterpret_cast<float4*>(p + D / 2 + 8 * sub);
+  a[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+  a[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+  b[0] = make_float4(x[4].x, x[4].y, x[5].x, x[5].y);
+  b[1] = make_float4(x[6].x, x[6].y, x[7].x, x[7].y);
+}
+
+// The 8 (c, s) of this lane's pairs, laid out for rotate(): Half: cs[j] belongs to
+// the features x[j] and x[4 + j]; interleaved: to the pair x[2j], x[2j + 1] split
+// as c[j].x for x[2j], c[j].y for x[2j + 1].
+template <int D, bool kInter>
+__device__ __forceinline__ void load_angles(const float* __restrict__ cos_t, const float* __restrict__ sin_t, int pos,
+                                            int sub, float2 (&c)[4], float2 (&s)[4]) {
+  const size_t row = static_cast<size_t>(pos) * (D / 2);
+  const int o0 = kInter ? 4 * sub : 8 * sub;
+  const int o1 = kInter ? D / 4 + 4 * sub : 8 * sub + 4;
+  const float4 c0 = __ldg(reinterpret_cast<const float4*>(cos_t + row + o0));
+  const float4 c1 = __ldg(reinterpret_cast<const float4*>(cos_t + row + o1));
+  const float4 s0 = __ldg(reinterpret_cast<const float4*>(sin_t + row + o0));
+  const float4 s1 = __ldg(reinterpret_cast<const float4*>(sin_t + row + o1));
+  c[0] = make_float2(c0.x, c0.y);
+  c[1] = make_float2(c0.z, c0.w);
+  c[2] = make_float2(c1.x, c1.y);
+  c[3] = make_float2(c1.z, c1.w);
+  s[0] = make_float2(s0.x, s0.y);
+  s[1] = make_float2(s0.z, s0.w);
+  s[2] = make_float2(s1.x, s1.y);
+  s[3] = make_float2(s1.z, s1.w);
+}
+
+// The rotation (kBack: its transpose) with a gain folded into the angles:
+// out = R diag(w) x.  Half: x[j] (first) and x[4 + j] (second), two pairs at a
+// time; interleaved: x[j] = (first, second) of pair j.
+//   Half:  out[j] = x[j] ca[j] - x[4+j] sb[j], out[4+j] = x[4+j] cb[j] + x[j] sa[j]
+//   with ca = c w_first, sb = s w_second, cb = c w_second, sa = s w_first
+//   interleaved: out[j] = x[j] * (c w0, c w1) + swap(x[j]) * (-s w1, s w0)
+struct Coef {
+  float2 p[8], q[8];  // Half: p = ca | cb, q = -sb | sa;  interleaved: p = (c w0, c w1), q = (-s w1, s w0)
+};
+
+template <bool kInter, bool kNorm>
+__device__ __forceinline__ void make_coef(const float2 (&c)[4], const float2 (&s)[4], const float2 (&w)[8], Coef& k) {
+  if constexpr (kInter) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float cj = (j & 1) ? c[j >> 1].y : c[j >> 1].x;
+      const float sj = (j & 1) ? s[j >> 1].y : s[j >> 1].x;
+      k.p[j] = kNorm ? make_float2(cj * w[j].x, cj * w[j].y) : make_float2(cj, cj);
+      k.q[j] = kNorm ? make_float2(-sj * w[j].y, sj * w[j].x) : make_float2(-sj, sj);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      k.p[j] = kNorm ? fmul2(c[j], w[j]) : c[j];
+      k.p[4 + j] = kNorm ? fmul2(c[j], w[4 + j]) : c[j];
+      const float2 ns = make_float2(-s[j].x, -s[j].y);
+      k.q[j] = kNorm ? fmul2(ns, w[4 + j]) : ns;
+      k.q[4 + j] = kNorm ? fmul2(s[j], w[j]) : s[j];
+    }
+  }
+}
+
+template <bool kInter>
+__device__ __forceinline__ void rotate(const float2 (&x)[8], const Coef& k, float2 (&o)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float2 other = kInter ? make_float2(x[j].y, x[j].x) : x[j < 4 ? j + 4 : j - 4];
+    o[j] = ffma2(x[j], k.p[j], fmul2(other, k.q[j]));
+  }
+}
+
+// gr = R^T g (no gain)
+template <bool kInter>
+__device__ __forceinline__ void rotate_back(const float2 (&g)[8], const float2 (&c)[4], const float2 (&s)[4],
+                                            float2 (&o)[8]) {
+  if constexpr (kInter) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float cj = (j & 1) ? c[j >> 1].y : c[j >> 1].x;
+      const float sj = (j & 1) ? s[j >> 1].y : s[j >> 1].x;
+      o[j].x = fmaf(g[j].x, cj, g[j].y * sj);
+      o[j].y = fmaf(g[j].y, cj, -g[j].x * sj);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      o[j] = ffma2(g[j], c[j], fmul2(g[4 + j], s[j]));
+      o[4 + j] = ffma2(g[4 + j], c[j], fmul2(g[j], make_float2(-s[j].x, -s[j].y)));
+    }
+  }
+}
+
+// this lane's 16 gains in the order of x
+template <int D>
+__device__ __forceinline__ void load_gain(const void* w, int w_f32, int sub, float2 (&o)[8]) {
+  if (w_f32) {
+    Raw<float> r;
+    load_row<D>(r, static_cast<const float*>(w), sub);
+    unpack(r, o);
+  } else {
+    Raw<__nv_bfloat16> r;
+    load_row<D>(r, static_cast<const __nv_bfloat16*>(w), sub);
+    unpack(r, o);
+  }
+}
+
+// sum over the d / 16 lanes of a row
+template <int D>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = D / 32; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <int D>
+__device__ __forceinline__ float row_rsqrt(const float2 (&x)[8], float eps) {
+  float2 q = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) q = ffma2(x[j], x[j], q);
+  return rsqrtf(fmaf(row_sum<D>(q.x + q.y), 1.f / D, eps));
+}
+
+// position of a token: -1 for padding; one outside the tables is reported and treated as padding
+__device__ __forceinline__ int token_position(const RopeArgs& a, int token, int n, int lane) {
+  int pos = a.positions ? a.positions[token] : n;
+  if (pos >= a.table) {
+    if (lane == 0) atomicCAS(a.status, 0, kDevBadInput | 0xD3);
+    pos = -1;
+  }
+  return pos;
+}
+
+// ---------------------------------------------------------------------------
+// Forward: a warp takes `per` groups of rows (4 heads of d = 128, 8 of d = 64)
+// of one tensor at one position; grid (position blocks, head groups of q then k).
+// ---------------------------------------------------------------------------
+template <typename T, int D, bool kNorm, bool kInter>
+__global__ void __launch_bounds__(kWarps * 32) rope_fwd_kernel(const RopeArgs a) {
+  constexpr int kLanes = D / 16;
+  constexpr int kRows = 32 / kLanes;
+  const int lane = lane_id();
+  const int token = blockIdx.x * kWarps + warp_id();
+  if (token >= a.tokens) return;
+  const int sub = lane % kLanes;
+  const bool is_q = static_cast<int>(blockIdx.y) < a.q_groups;
+  const int group = is_q ? blockIdx.y : blockIdx.y - a.q_groups;
+  const int nh = is_q ? a.H : a.Hkv;
+  const int h0 = group * a.per * kRows + lane / kLanes;
+  const int b = token / a.N, n = token - b * a.N;
+  const RopeTensor& t = is_q ? a.q : a.k;
+  const T* x0 = static_cast<const T*>(t.x) + b * t.sb + n * t.sn;
+  T* o0 = static_cast<T*>(t.out) + static_cast<size_t>(token) * nh * D;
+  const int pos = token_position(a, token, n, lane);
+  float2 c[4], s[4], w[8];
+  if (pos >= 0) load_angles<D, kInter>(a.cos_t, a.sin_t, pos, sub, c, s);
+  if (kNorm) load_gain<D>(t.w, a.w_f32, sub, w);
+  Coef k;
+  if (pos >= 0) make_coef<kInter, kNorm>(c, s, w, k);
+  for (int it = 0; it < a.per; it += 2) {
+    Raw<T> raw[2] = {};
+    const int ha = h0 + it * kRows, hb = ha + kRows;
+    const bool oka = ha < nh, okb = it + 1 < a.per && hb < nh;
+    if (pos >= 0) {
+      if (oka) load_row<D>(raw[0], x0 + ha * t.sh, sub);
+      if (okb) load_row<D>(raw[1], x0 + hb * t.sh, sub);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float2 o[8];
+      if (pos >= 0) {
+        float2 x[8];
+        unpack(raw[u], x);
+        float r = 1.f;
+        if constexpr (kNorm) r = row_rsqrt<D>(x, a.eps);  // every lane of the warp, its row valid or not
+        rotate<kInter>(x, k, o);
+        if constexpr (kNorm) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] = fmul2(o[j], make_float2(r, r));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = make_float2(0.f, 0.f);
+      }
+      if (u == 0 ? oka : okb) store_row<D>(o0 + static_cast<size_t>(u == 0 ? ha : hb) * D, sub, o);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward: blocks [0, q_blocks) walk the (position, head group) units of q, the
+// others those of k, each warp with its own running sum of the gain's gradient;
+// a block writes the sum of its warps to partial[block][d].
+// ---------------------------------------------------------------------------
+template <typename T, int D, bool kNorm, bool kInter>
+__global__ void __launch_bounds__(kWarps * 32) rope_bwd_kernel(const RopeArgs a) {
+  constexpr int kLanes = D / 16;
+  constexpr int kRows = 32 / kLanes;
+  const int lane = lane_id(), warp = warp_id();
+  const int sub = lane % kLanes;
+  const bool is_q = static_cast<int>(blockIdx.x) < a.q_blocks;
+  const int first = is_q ? blockIdx.x : blockIdx.x - a.q_blocks;
+  const int blocks = is_q ? a.q_blocks : static_cast<int>(gridDim.x) - a.q_blocks;
+  const int nh = is_q ? a.H : a.Hkv;
+  const int groups = is_q ? a.q_groups : a.k_groups;
+  const RopeTensor& t = is_q ? a.q : a.k;
+  const long long units = static_cast<long long>(a.tokens) * groups;
+  float2 w[8], acc[8];
+  if (kNorm) load_gain<D>(t.w, a.w_f32, sub, w);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) acc[j] = make_float2(0.f, 0.f);
+
+  for (long long u = static_cast<long long>(first) * kWarps + warp; u < units; u += static_cast<long long>(blocks) * kWarps) {
+    const int token = static_cast<int>(u / groups);
+    const int group = static_cast<int>(u - static_cast<long long>(token) * groups);
+    const int b = token / a.N, n = token - b * a.N;
+    const int pos = token_position(a, token, n, lane);
+    const T* x0 = static_cast<const T*>(t.x) + b * t.sb + n * t.sn;
+    const T* g0 = static_cast<const T*>(t.g) + b * t.gb + n * t.gn;
+    T* o0 = static_cast<T*>(t.out) + static_cast<size_t>(token) * nh * D;
+    float2 c[4], s[4];
+    if (pos >= 0) load_angles<D, kInter>(a.cos_t, a.sin_t, pos, sub, c, s);
+    for (int it = 0; it < a.per; ++it) {
+      const int h = (group * a.per + it) * kRows + lane / kLanes;
+      const bool ok = h < nh;
+      float2 o[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = make_float2(0.f, 0.f);
+      if (pos >= 0) {
+        Raw<T> rx = {}, rg = {};
+        if (ok) {
+          load_row<D>(rg, g0 + h * t.gh, sub);
+          if (kNorm) load_row<D>(rx, x0 + h * t.sh, sub);
+        }
+        float2 g[8], gr[8];
+        unpack(rg, g);
+        rotate_back<kInter>(g, c, s, gr);
+        if constexpr (!kNorm) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] = gr[j];
+        } else {
+          float2 x[8];
+          unpack(rx, x);
+          const float r = row_rsqrt<D>(x, a.eps);
+          float2 dot = make_float2(0.f, 0.f), gx[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            gx[j] = fmul2(gr[j], x[j]);
+            dot = ffma2(gx[j], w[j], dot);
+          }
+          const float m = row_sum<D>(dot.x + dot.y) * (1.f / D) * r * r * r;
+          const float2 r2 = make_float2(r, r), m2 = make_float2(-m, -m);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (ok) acc[j] = ffma2(gx[j], r2, acc[j]);
+            o[j] = ffma2(fmul2(gr[j], w[j]), r2, fmul2(x[j], m2));
+          }
+        }
+      }
+      if (ok) store_row<D>(o0 + static_cast<size_t>(h) * D, sub, o);
+    }
+  }
+
+  if constexpr (kNorm) {
+    __shared__ float sums[kWarps][D];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float2 v = acc[j];
+#pragma unroll
+      for (int o = kLanes; o < 32; o <<= 1) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+      }
+      if (lane < kLanes) {
+        const int f = (j < 4 ? 0 : D / 2) + 8 * sub + 2 * (j & 3);
+        sums[warp][f] = v.x;
+        sums[warp][f + 1] = v.y;
+      }
+    }
+    __syncthreads();
+    for (int f = threadIdx.x; f < D; f += kWarps * 32) {
+      float v = 0.f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) v += sums[i][f];
+      a.partial[static_cast<size_t>(blockIdx.x) * D + f] = v;
+    }
+  }
+}
+
+// dw = sum of the blocks' partial sums, in 64 bits and in a fixed order: block 0 for q, 1 for k
+template <int D>
+__global__ void __launch_bounds__(8 * D) rope_dw_kernel(const float* __restrict__ partial, int q_blocks, int blocks,
+                                                        void* dwq, void* dwk, int w_f32) {
+  __shared__ double sums[8][D];
+  const int f = threadIdx.x % D, part = threadIdx.x / D;
+  const int lo = blockIdx.x ? q_blocks : 0, hi = blockIdx.x ? blocks : q_blocks;
+  double v = 0.0;
+#pragma unroll 4
+  for (int i = lo + part; i < hi; i += 8) v += static_cast<double>(partial[static_cast<size_t>(i) * D + f]);
+  sums[part][f] = v;
+  __syncthreads();
+  if (part == 0) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) v += sums[i][f];
+    void* out = blockIdx.x ? dwk : dwq;
+    if (w_f32)
+      static_cast<float*>(out)[f] = static_cast<float>(v);
+    else
+      static_cast<__nv_bfloat16*>(out)[f] = __float2bfloat16_rn(static_cast<float>(v));
+  }
+}
+
+template <typename T, int D>
+cudaError_t launch_fwd_d(const RopeArgs& a, cudaStream_t s) {
+  const dim3 grid((a.tokens + kWarps - 1) / kWarps, a.q_groups + a.k_groups);
+  const bool norm = a.q.w != nullptr;
+  if (norm && a.interleaved) rope_fwd_kernel<T, D, true, true><<<grid, kWarps * 32, 0, s>>>(a);
+  else if (norm) rope_fwd_kernel<T, D, true, false><<<grid, kWarps * 32, 0, s>>>(a);
+  else if (a.interleaved) rope_fwd_kernel<T, D, false, true><<<grid, kWarps * 32, 0, s>>>(a);
+  else rope_fwd_kernel<T, D, false, false><<<grid, kWarps * 32, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_bwd_d(const RopeArgs& a, cudaStream_t s) {
+  const bool norm = a.q.w != nullptr;
+  if (a.blocks == 0) {  // no row: the gains' gradients are still written (zero)
+  } else if (norm && a.interleaved) rope_bwd_kernel<T, D, true, true><<<a.blocks, kWarps * 32, 0, s>>>(a);
+  else if (norm) rope_bwd_kernel<T, D, true, false><<<a.blocks, kWarps * 32, 0, s>>>(a);
+  else if (a.interleaved) rope_bwd_kernel<T, D, false, true><<<a.blocks, kWarps * 32, 0, s>>>(a);
+  else rope_bwd_kernel<T, D, false, false><<<a.blocks, kWarps * 32, 0, s>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !norm) return e;
+  rope_dw_kernel<D><<<2, 8 * D, 0, s>>>(a.partial, a.q_blocks, a.blocks, a.dwq, a.dwk, a.w_f32);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_rope_fwd(const RopeArgs& a, int d, bool f32, cudaStream_t s) {
+  if (f32) return d == 128 ? launch_fwd_d<float, 128>(a, s) : launch_fwd_d<float, 64>(a, s);
+  return d == 128 ? launch_fwd_d<__nv_bfloat16, 128>(a, s) : launch_fwd_d<__nv_bfloat16, 64>(a, s);
+}
+
+cudaError_t launch_rope_bwd(const RopeArgs& a, int d, bool f32, cudaStream_t s) {
+  if (f32) return d == 128 ? launch_bwd_d<float, 128>(a, s) : launch_bwd_d<float, 64>(a, s);
+  return d == 128 ? launch_bwd_d<__nv_bfloat16, 128>(a, s) : launch_bwd_d<__nv_bfloat16, 64>(a, s);
+}
+
+}  // namespace fa

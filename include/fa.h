@@ -335,6 +335,121 @@ int fa_decode_paged(const void* Q, const void* K_cache, const void* V_cache, con
  * arguments are invalid). */
 size_t fa_decode_workspace_size(int B, int H, int Hkv, int d, int page_size, int max_pages);
 
+/*
+ * RMS norm of every query and key head and the rotation by position, in one pass
+ * (what models put between their projections and the attention; the pages have
+ * no counterpart).  For each row x of d features, with r = 1 / sqrt(mean(x^2) + eps)
+ * and the gain w of its tensor, y = x * r * w, and for each pair (first, second) of
+ * features with the angle (c, s) of the row's position
+ *     out_first = y_first * c - y_second * s,   out_second = y_second * c + y_first * s.
+ *   Q, K         [B, N, H, d] and [B, N, Hkv, d] of dtype.  q_strides / k_strides:
+ *                NULL for dense tensors, else host arrays of the (batch, position,
+ *                head) strides in elements, multiples of 16 bytes; the features are
+ *                contiguous.  So slices of a packed projection are read in place.
+ *                H or Hkv may be 0 (that tensor is not touched).  H and Hkv are
+ *                independent here.
+ *   q_weight,    [d] gains of weight_dtype, or both NULL: no norm, the rotation alone
+ *   k_weight     (eps is then not used).
+ *   cos_table,   [table_rows, d/2] fp32, dense: row p holds the d/2 cosines and sines
+ *   sin_table    of position p.
+ *   positions    [B, N] int32 device array, or NULL: 0 .. N - 1 (N <= table_rows then).
+ *                A negative position marks padding: its rows are written as zeros and
+ *                its inputs are not read.  A position >= table_rows is treated the same
+ *                and makes the next fa_last_device_status() return FA_ERR_DEVICE_INPUT
+ *                (detail 0x2000 | 0xD3).
+ *   Q_out, K_out dense outputs of dtype; must not overlap any input.
+ *   interleaved  0: pairs (i, i + d/2); 1: pairs (2i, 2i + 1).
+ *   dtype, weight_dtype  FA_BF16 or FA_FP32 each; all arithmetic is fp32, each output is
+ *                rounded once.
+ *   d            64 or 128.  B * N < 2^31.
+ */
+int fa_qk_norm_rope(const void* Q, const void* K, const void* q_weight, const void* k_weight, const float* cos_table,
+                    const float* sin_table, const int* positions, void* Q_out, void* K_out, int B, int N, int H,
+                    int Hkv, int d, const long long* q_strides, const long long* k_strides, int table_rows, float eps,
+                    int interleaved, int dtype, int weight_dtype, void* stream);
+
+/*
+ * Its backward.  Q, K, the gains, tables, positions and flags as the forward had
+ * them; dQ_out, dK_out the gradients of its outputs (strides as above).  Writes dQ,
+ * dK (dense, dtype; zeros where padding is) and, with gains, dq_weight and dk_weight
+ * ([d] of weight_dtype; sums over all rows in a fixed order: the same call gives
+ * the same bits).  The tables get no gradient.
+ *   workspace    device buffer of fa_qk_norm_rope_workspace_size(d) bytes, 256-byte
+ *                aligned, overwritten; not needed (NULL) without gains.
+ */
+int fa_qk_norm_rope_bwd(const void* Q, const void* K, const void* q_weight, const void* k_weight,
+                        const float* cos_table, const float* sin_table, const int* positions, const void* dQ_out,
+                        const void* dK_out, void* dQ, void* dK, void* dq_weight, void* dk_weight, int B, int N, int H,
+                        int Hkv, int d, const long long* q_strides, const long long* k_strides,
+                        const long long* dq_out_strides, const long long* dk_out_strides, int table_rows, float eps,
+                        int interleaved, int dtype, int weight_dtype, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/* Workspace bytes of fa_qk_norm_rope_bwd (0 for an unsupported d). */
+size_t fa_qk_norm_rope_workspace_size(int d);
+
+/*
+ * Write new tokens' K and V rows into a paged KV cache (the pools and block table of
+ * fa_decode_paged; "Flash Attention" (Ultralytics glossary), "Flash Attention и
+ * смежные понятия", PagedAttention).
+ *   K, V         [B, N, Hkv, d] bf16 rows; k_strides / v_strides as in fa_qk_norm_rope.
+ *   K_cache,     [num_pages, page_size, Hkv, d], bf16 (fp8 = 0) or e4m3 codes (fp8 = 1).
+ *   V_cache      Row n of sequence b becomes its position start[b] + n.
+ *   kv_scale     fp8: [num_pages, Hkv, 2, page_size] bytes, the scale of every row (K's,
+ *                then V's): byte e + 127 stands for 2^e.  NULL for bf16 pools.
+ *   start        [B] int32 device array: the positions already cached.
+ *   count        [B] int32 device array of the rows to write of each sequence (0 .. N), or
+ *                NULL: all N.  Rows past it are not read, and nothing else is written.
+ * 8-bit rows: e is the smallest integer >= -126 with max|x| <= 448 * 2^e, the codes are
+ * x / 2^e rounded to the nearest (ties to even).  A row with an Inf or a NaN gets the
+ * scale byte 255 (NaN) and reads back as NaN.
+ * The kernel checks the device data: a sequence whose start or count is out of range
+ * (start + count <= max_pages * page_size), or a row whose page is no page of the pool,
+ * is left out, and the next fa_last_device_status() returns FA_ERR_DEVICE_INPUT.  Two
+ * rows of a call must not share a slot (two sequences with a page in common): which
+ * one is kept, and whether whole, is not specified.
+ *   page_size a power of two from 8 to 4096, d 64 or 128 (FA_ERR_UNSUPPORTED otherwise);
+ *   num_pages * page_size < 2^31, max_pages * page_size <= 2^30, B, Hkv <= 65535.
+ */
+int fa_cache_append(const void* K, const void* V, void* K_cache, void* V_cache, void* kv_scale, const int* block_table,
+                    const int* start, const int* count, int B, int N, int Hkv, int d, const long long* k_strides,
+                    const long long* v_strides, int page_size, int num_pages, int max_pages, int fp8, void* stream);
+
+/*
+ * Read the first N positions of every sequence back out of a paged KV cache.
+ *   K, V         dense [B, N, Hkv, d] bf16 outputs, written completely: position j of
+ *                sequence b for j < seqlens[b] (8-bit rows: code * scale, rounded to bf16),
+ *                zeros from there on.
+ * Other arguments as fa_cache_append.  A length outside [0, max_pages * page_size] gives
+ * zeros, and so does a position whose page is no page of the pool; both are reported.
+ */
+int fa_cache_read(const void* K_cache, const void* V_cache, const void* kv_scale, const int* block_table,
+                  const int* seqlens, void* K, void* V, int B, int N, int Hkv, int d, int page_size, int num_pages,
+                  int max_pages, int fp8, void* stream);
+
+/*
+ * One decode step over a paged 8-bit KV cache: fa_decode_paged with the pools and scale
+ * bytes of fa_cache_append (fp8 = 1).  The result is the exact attention of the
+ * dequantised rows; the probabilities (times the V scales) are rounded to f16 before
+ * P V, sums and statistics are fp32.
+ *   window_left  -1: every cached position is visible; else the query (the sequence's
+ *                last position) sees itself and the window_left positions before it, and
+ *                pages wholly before those are neither looked up nor loaded.
+ *   workspace    as fa_decode_paged, with fa_decode_fp8_workspace_size() bytes.
+ * A row whose scale byte is 255 makes the heads that see it NaN.  The codes 0x7f and
+ * 0xff, which fa_cache_append writes only in such rows, count as +-480 in a row with
+ * another scale byte.  Out-of-range lengths and page indices leave the sequence's rows
+ * empty (O = 0, LSE = -inf) and are reported, as in fa_decode_paged.
+ *   max_pages * page_size <= 2^30; the other limits as fa_decode_paged.
+ */
+int fa_decode_paged_fp8(const void* Q, const void* K_cache, const void* V_cache, const void* kv_scale,
+                        const int* block_table, const int* seqlens, void* O, float* LSE, int B, int H, int Hkv, int d,
+                        int page_size, int num_pages, int max_pages, float scale, int window_left, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Workspace bytes with which fa_decode_paged_fp8 splits as it would unconstrained. */
+size_t fa_decode_fp8_workspace_size(int B, int H, int Hkv, int d, int page_size, int max_pages, int window_left);
+
 /* Static English text for a status code. */
 const char* fa_status_string(int status);
 

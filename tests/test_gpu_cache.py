@@ -1,0 +1,260 @@
+"""Writing and reading a paged cache: exact against the oracle.
+
+The 8-bit format has no freedom (a power-of-two scale, x / scale exact, one
+rounding to the nearest code), so codes, scale bytes and everything that was
+not to be written are compared bit by bit; so are the rows read back, code *
+scale rounded once to bf16.
+"""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import exact_io_aware_51_b200 as fa
+from oracle import serving as S
+from tests.helpers import need_gpu
+
+
+def _table(need, page, spare, width, g):
+    n = [(x + page - 1) // page for x in need]
+    total = sum(n) + spare
+    order = torch.randperm(total, generator=g).to(torch.int32)
+    table = torch.full((len(n), max([width] + n)), -1, dtype=torch.int32)
+    at = 0
+    for b, k in enumerate(n):
+        table[b, :k] = order[at:at + k]
+        at += k
+    return table, total
+
+
+def _pool(pages, page, Hkv, d, fp8, g):
+    shape = (pages, page, Hkv, d)
+    if fp8:
+        kc, vc = (torch.randint(0, 256, shape, generator=g, dtype=torch.uint8) for _ in range(2))
+        return kc, vc, torch.randint(0, 256, (pages, Hkv, 2, page), generator=g, dtype=torch.uint8)
+    return *(torch.randn(shape, generator=g).to(torch.bfloat16) for _ in range(2)), None
+
+
+def _rows(shape, g):
+    """Rows of very different sizes, bf16."""
+    x = torch.randn(shape, generator=g) * torch.exp2(torch.randint(-12, 12, (*shape[:-1], 1), generator=g).float())
+    return x.to(torch.bfloat16)
+
+
+CASES = [
+    # fp8, B, N, Hkv, d, page, starts, counts, packed
+    (True, 3, 1, 8, 128, 16, [0, 15, 16], None, False),
+    (True, 2, 37, 3, 64, 8, [5, 0], [37, 11], True),
+    (True, 2, 130, 1, 128, 64, [1, 63], [130, 0], False),
+    (True, 4, 9, 5, 64, 4096, [0, 4095, 100, 8000], [9, 9, 1, 5], True),
+    (True, 1, 300, 2, 128, 32, [7], None, True),
+    (False, 3, 1, 4, 64, 16, [0, 31, 32], None, False),
+    (False, 2, 41, 3, 128, 8, [3, 0], [40, 7], True),
+]
+
+
+def _name(c):
+    return f"{'fp8' if c[0] else 'bf16'}-B{c[1]}N{c[2]}kv{c[3]}d{c[4]}P{c[5]}"
+
+
+def _make(case, seed):
+    fp8, B, N, Hkv, d, page, starts, counts, packed = case
+    g = torch.Generator().manual_seed(seed)
+    counts_ = [N] * B if counts is None else counts
+    table, pages = _table([s + c for s, c in zip(starts, counts_)], page, 2, 3, g)
+    kc, vc, sc = _pool(pages, page, Hkv, d, fp8, g)
+    if packed:
+        x = _rows((B, N, 2 + 2 * Hkv, d), g).cuda()
+        k, v = x[:, :, 2:2 + Hkv], x[:, :, 2 + Hkv:]
+    else:
+        k, v = _rows((B, N, Hkv, d), g).cuda(), _rows((B, N, Hkv, d), g).cuda()
+    start = torch.tensor(starts, dtype=torch.int32)
+    count = None if counts is None else torch.tensor(counts, dtype=torch.int32)
+    return k, v, kc, vc, sc, table, start, count
+
+
+def _np(t):
+    return None if t is None else (t.double().numpy() if t.dtype == torch.bfloat16 else t.numpy())
+
+
+def _c(t):
+    return None if t is None else t.cuda()
+
+
+def _same_pool(got, ref, fp8):
+    a = got.cpu()
+    assert np.array_equal(a.numpy() if fp8 else a.double().numpy(), ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", CASES, ids=_name)
+def test_append_and_read_match_oracle(case):
+    need_gpu()
+    fp8, B, N, Hkv, d, page = case[:6]
+    k, v, kc, vc, sc, table, start, count = _make(case, seed=31)
+    rk, rv, rs = S.cache_append(k.cpu().double(), v.cpu().double(), _np(kc), _np(vc), table, start, _np(sc), count)
+    gk, gv, gs = kc.cuda(), vc.cuda(), _c(sc)
+    assert fa.cache_append(k, v, gk, gv, table.cuda(), start.cuda(), kv_scale=gs, count=_c(count)) is None
+    assert fa.last_device_status()[0] == 0
+    _same_pool(gk, rk, fp8)
+    _same_pool(gv, rv, fp8)
+    if fp8:
+        assert np.array_equal(gs.cpu().numpy(), rs)
+    # read back: the appended length, a length past every end, and one position
+    lens = start + (N if count is None else count)
+    K, V = S.dequantise_cache(rk, rv, rs) if fp8 else (rk, rv)
+    for length in (int(lens.max()) + 3, 1):
+        out = fa.cache_read(gk, gv, table.cuda(), lens.cuda(), length, kv_scale=gs)
+        for got, pool in zip(out, (K, V)):
+            ref = torch.from_numpy(S.cache_read(pool, table, lens, length)).to(torch.bfloat16)
+            assert torch.equal(torch.nan_to_num(got.cpu().float(), nan=12345.0),
+                               torch.nan_to_num(ref.float(), nan=12345.0))
+    assert fa.last_device_status()[0] == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_at_the_formats_edges(d):
+    """Zero rows, subnormals, the largest bf16, rows on each side of a power of two's 448, every tie, Inf and NaN."""
+    need_gpu()
+    vals = torch.from_numpy(S.e4m3_values()[:127]).float()
+    ties = (vals[1:] + vals[:-1]) / 2
+    big = torch.finfo(torch.bfloat16).max
+    heads = [torch.zeros(d), torch.full((d,), 2.0 ** -133), torch.full((d,), -2.0 ** -126), torch.full((d,), big),
+             torch.cat([vals, vals[-1:]])[-d:], torch.cat([torch.tensor([448.0, 448.0]), ties])[:d],
+             torch.cat([torch.tensor([448.0, 448.0]), -ties])[-d:], torch.linspace(-448, 448, d), torch.linspace(-450, 450, d),
+             torch.linspace(-1, 1, d) * 2.0 ** -120, torch.full((d,), -0.0)]
+    for bad in (float("inf"), float("-inf"), float("nan")):
+        x = torch.linspace(-2, 2, d)
+        x[d // 3] = bad
+        heads.append(x)
+    rows = torch.stack(heads).to(torch.bfloat16).reshape(1, 1, len(heads), d)
+    Hkv, page = len(heads), 8
+    kc = torch.zeros((1, page, Hkv, d), dtype=torch.uint8)
+    sc = torch.zeros((1, Hkv, 2, page), dtype=torch.uint8)
+    table, start = torch.zeros((1, 1), dtype=torch.int32), torch.tensor([3], dtype=torch.int32)
+    v = rows.flip(2)
+    rk, rv, rs = S.cache_append(rows.double(), v.double(), kc.numpy(), kc.numpy(), table, start, sc.numpy())
+    gk, gv, gs = kc.cuda(), kc.clone().cuda(), sc.cuda()
+    fa.cache_append(rows.cuda(), v.cuda(), gk, gv, table.cuda(), start.cuda(), kv_scale=gs)
+    assert np.array_equal(gs.cpu().numpy(), rs)
+    finite = rs[0, :, 0, 3] != 255
+    assert np.array_equal(gk.cpu().numpy()[0, 3][finite], rk[0, 3][finite])
+    assert np.all(gk.cpu().numpy()[0, 3][~finite] & 127 == 127)      # NaN codes
+    out, _ = fa.cache_read(gk, gv, table.cuda(), start.cuda() + 1, 4, kv_scale=gs)
+    ref = torch.from_numpy(S.dequantise_cache(rk, rv, rs)[0][0, 3]).to(torch.bfloat16)
+    got = out[0, 3].cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(ref)) and bool((torch.isnan(got).any(-1).numpy() == ~finite).all())
+    assert torch.equal(got[torch.from_numpy(finite)], ref[torch.from_numpy(finite)])
+
+
+@pytest.mark.gpu
+def test_float8_tensors_and_codes_are_one_format():
+    need_gpu()
+    case = (True, 2, 20, 2, 64, 16, [0, 9], None, False)
+    k, v, kc, vc, sc, table, start, _ = _make(case, seed=32)
+    a = [t.cuda() for t in (kc, vc, sc)]
+    b = [kc.cuda().view(torch.float8_e4m3fn), vc.cuda().view(torch.float8_e4m3fn), sc.cuda().view(torch.float8_e8m0fnu)]
+    for x in (a, b):
+        fa.cache_append(k, v, x[0], x[1], table.cuda(), start.cuda(), kv_scale=x[2])
+    for x, y in zip(a, b):
+        assert torch.equal(x, y.view(torch.uint8))
+    lens = start.cuda() + 20
+    for x, y in zip(fa.cache_read(a[0], a[1], table.cuda(), lens, 29, kv_scale=a[2]),
+                    fa.cache_read(b[0], b[1], table.cuda(), lens, 29, kv_scale=b[2])):
+        assert torch.equal(x.view(torch.int16), y.view(torch.int16))
+    # the scale bytes are the values of torch's 8-bit exponent type
+    pos = int(start[1])
+    pg = int(table[1, pos // 16])
+    row = a[0][pg, pos % 16, 1].view(torch.float8_e4m3fn).float() * b[2][pg, 1, 0, pos % 16].float()
+    assert torch.equal(row, fa.cache_read(a[0], a[1], table.cuda(), lens, 29, kv_scale=a[2])[0][1, pos, 1].float())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [True, False])
+def test_bad_device_data_is_reported_and_left_out(fp8):
+    need_gpu()
+    case = (fp8, 3, 12, 2, 64, 8, [4, 0, 9], [12, 5, 7], False)
+    k, v, kc, vc, sc, table, start, count = _make(case, seed=33)
+    pages = kc.shape[0]
+
+    def append(table, start, count):
+        pools = [kc.cuda(), vc.cuda(), _c(sc)]
+        fa.last_device_status()
+        fa.cache_append(k, v, pools[0], pools[1], table.cuda(), start.cuda(), kv_scale=pools[2], count=count.cuda())
+        return pools, fa.last_device_status()
+
+    def expect(b_out, table, pools, skip=()):
+        c = count.clone()
+        c[b_out] = 0
+        ref = S.cache_append(k.cpu().double(), v.cpu().double(), _np(kc), _np(vc), table, start, _np(sc), c)
+        got = [p if p is None else p.cpu() for p in pools]
+        for g, r in zip(got, ref):
+            if r is not None:
+                assert np.array_equal(g.numpy() if fp8 else g.double().numpy(), r)
+
+    for what, value in (("start", -1), ("start", table.shape[1] * 8 - 11), ("count", 13), ("count", -1)):
+        s, c = start.clone(), count.clone()
+        (s if what == "start" else c)[0] = value
+        pools, (rc, detail) = append(table, s, c)
+        assert rc == -9 and detail == 0x2000 | 0xD1, (what, value)
+        expect(0, table, pools)
+    for page in (pages, -5):
+        t = table.clone()
+        t[1, 0] = page
+        pools, (rc, detail) = append(t, start, count)
+        assert rc == -9 and detail == 0x2000 | 0xD2
+        expect(1, table, pools)
+    # reads: a bad length gives zeros, a bad page zeros for its positions
+    lens = (start + count).cuda()
+    pools = [kc.cuda(), vc.cuda(), _c(sc)]
+    clean = fa.cache_read(*pools[:2], table.cuda(), lens, 20, kv_scale=pools[2])
+    for bad in (-1, table.shape[1] * 8 + 1):
+        l2 = lens.clone()
+        l2[2] = bad
+        out = fa.cache_read(*pools[:2], table.cuda(), l2, 20, kv_scale=pools[2])
+        assert fa.last_device_status()[0] == -9
+        assert torch.count_nonzero(out[0][2].view(torch.int16)) == 0
+        assert torch.equal(out[0][:2].view(torch.int16), clean[0][:2].view(torch.int16))
+    t = table.clone()
+    t[0, 1] = pages + 7
+    out = fa.cache_read(*pools[:2], t.cuda(), lens, 20, kv_scale=pools[2])
+    assert fa.last_device_status() == (-9, 0x2000 | 0xD2)
+    assert torch.count_nonzero(out[1][0, 8:16].view(torch.int16)) == 0
+    assert torch.equal(out[1][0, :8].view(torch.int16), clean[1][0, :8].view(torch.int16))
+    assert fa.last_device_status()[0] == 0
+
+
+@pytest.mark.gpu
+def test_table_entries_past_the_end_are_not_read():
+    """A table holds what it likes behind a sequence's last page, and padded rows what they like."""
+    need_gpu()
+    case = (True, 2, 10, 2, 64, 8, [0, 3], [4, 10], False)
+    k, v, kc, vc, sc, table, start, count = _make(case, seed=34)
+    k, v = k.clone(), v.clone()
+    k[0, 4:], v[0, 4:] = float("nan"), float("nan")
+    gk, gv, gs = kc.cuda(), vc.cuda(), sc.cuda()
+    wide = torch.full((2, 8), 2 ** 30, dtype=torch.int32)
+    wide[0, :1], wide[1, :2] = table[0, :1], table[1, :2]
+    fa.cache_append(k, v, gk, gv, wide.cuda(), start.cuda(), kv_scale=gs, count=count.cuda())
+    fa.cache_read(gk, gv, wide.cuda(), (start + count).cuda(), 64, kv_scale=gs)
+    assert fa.last_device_status()[0] == 0
+    ref = S.cache_append(k.nan_to_num(0).cpu().double(), v.nan_to_num(0).cpu().double(), _np(kc), _np(vc), table, start, _np(sc), count)
+    assert np.array_equal(gk.cpu().numpy(), ref[0]) and np.array_equal(gs.cpu().numpy(), ref[2])
+
+
+@pytest.mark.gpu
+def test_empty_calls():
+    need_gpu()
+    kc = torch.zeros((2, 8, 2, 64), dtype=torch.uint8, device="cuda")
+    sc = torch.zeros((2, 2, 2, 8), dtype=torch.uint8, device="cuda")
+    for B, N in ((0, 3), (2, 0)):
+        k = torch.zeros((B, N, 2, 64), dtype=torch.bfloat16, device="cuda")
+        bt = torch.zeros((B, 1), dtype=torch.int32, device="cuda")
+        st = torch.zeros((B,), dtype=torch.int32, device="cuda")
+        fa.cache_append(k, k, kc, kc, bt, st, kv_scale=sc)
+        out = fa.cache_read(kc, kc, bt, st, N, kv_scale=sc)
+        assert out[0].shape == (B, N, 2, 64)
+    assert torch.count_nonzero(kc) == 0

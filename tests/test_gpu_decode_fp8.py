@@ -1,0 +1,263 @@
+"""Decode over the paged 8-bit cache: the CUDA kernels against the fp64 oracle on the dequantised rows.
+
+Tolerance of an output element: half a bf16 step, 2^-8 of it; and, against sum_j p_j |v_j|
+(the oracle run on |V|): the f16 rounding of P times the V scale, 2^-11; the
+fp32 sums and ex2 (2 units), under 2^-16; and e^delta - 1 for an error delta of the scores, which
+moves a probability and the denominator, so 2 delta.  delta: fp32 accumulation of d = 128 products
+on the tensor cores, 2^-23 of the magnitudes each: 2^-16 scale sum |q k|, with ex2's own argument rounding
+(2^-24 of the score) far below.  Doubled once for the second-order terms.
+LSE: delta + 2^-18 (1 + |LSE|) + the fp32 sum of the row's p, 2^-24 for each of L / 32 + 64 steps.
+"""
+
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import exact_io_aware_51_b200 as fa
+from exact_io_aware_51_b200 import inputs as I
+from oracle import serving as S
+from tests.helpers import need_gpu
+
+
+def _make(B, H, Hkv, d, P, lens, seed, spare=2, max_pages=None, spread=1.0, poison=True):
+    """q, codes, scales, table, lens on the CPU; unused rows hold NaN codes and NaN scales."""
+    q, k, v, table, sl = I.make_paged_decode(B, H, Hkv, d, P, lens, seed=seed, spare_pages=spare, max_pages=max_pages)
+    g = torch.Generator().manual_seed(seed + 1)
+    k, v = (t.float() * torch.exp(spread * torch.randn((*t.shape[:3], 1), generator=g)) for t in (k, v))
+    kc, kb = S.quantise_rows(k.to(torch.bfloat16).double().numpy())
+    vc, vb = S.quantise_rows(v.to(torch.bfloat16).double().numpy())
+    if poison:
+        used = np.zeros(k.shape[:2], bool)
+        for b, n in enumerate(lens):
+            for j in range(n):
+                used[int(table[b, j // P]), j % P] = True
+        for c, s in ((kc, kb), (vc, vb)):
+            c[~used], s[~used] = 0xFF, 255
+    sc = np.stack([np.moveaxis(kb, 1, 2), np.moveaxis(vb, 1, 2)], axis=2)
+    return q, torch.from_numpy(kc), torch.from_numpy(vc), torch.from_numpy(np.ascontiguousarray(sc)), table, sl
+
+
+def _check(args, o, lse, scale, window=None, skip=()):
+    q, kc, vc, sc, table, sl = args
+    K, V = S.dequantise_cache(kc, vc, sc)
+    ro, rl = S.decode_window(q.double(), K, V, table, sl, scale, window)
+    mo, _ = S.decode_window(q.double(), K, np.abs(V), table, sl, scale, window)
+    P = kc.shape[1]
+    o, lse = o.cpu().double().numpy(), lse.cpu().double().numpy()
+    for b, n in enumerate(int(x) for x in sl):
+        if b in skip:
+            continue
+        if n == 0:
+            assert np.all(o[b] == 0) and np.all(np.isneginf(lse[b]))
+            continue
+        lo = 0 if window is None else max(0, n - 1 - window)
+        at = np.arange(lo, n)
+        k = np.abs(K[table[b, at // P].numpy(), at % P])                       # [n, Hkv, d]
+        a = np.abs(q[b].double().numpy()).reshape(k.shape[1], -1, k.shape[2])  # [Hkv, G, d]
+        delta = 2.0 ** -16 * scale * np.einsum("hgd,nhd->hgn", a, k).max(-1).reshape(-1)
+        tol = 2.0 ** -8 * np.abs(ro[b]) + 2 * (2.0 ** -11 + 2.0 ** -16 + 2 * delta[:, None]) * mo[b] + 1e-30
+        assert np.all(np.abs(o[b] - ro[b]) <= tol), b
+        assert np.all(np.abs(lse[b] - rl[b]) <= delta + 2.0 ** -18 * (1 + np.abs(rl[b])) + 2.0 ** -24 * (n / 32 + 64)), b
+
+
+def _run(args, **kw):
+    q, kc, vc, sc, table, sl = (t.cuda() for t in args)
+    o, lse = fa.decode_paged_fp8(q, kc, vc, sc, table, sl, **kw)
+    assert fa.last_device_status()[0] == 0
+    return o, lse
+
+
+CASES = [
+    # B, H, Hkv, d, page, lengths, window
+    (4, 8, 2, 128, 16, [1, 17, 64, 200], None),
+    (3, 16, 16, 64, 8, [0, 65, 130], None),
+    (2, 32, 1, 128, 64, [300, 129], None),          # 32 query heads on one K/V head: two head groups
+    (2, 64, 8, 128, 256, [1000, 513], None),
+    (2, 32, 2, 64, 32, [63, 777], None),            # 16 query heads per K/V head: two column blocks
+    (1, 4, 4, 64, 4096, [5000], None),
+    (5, 12, 4, 128, 128, [128, 129, 0, 255, 1], None),
+    (2, 9, 1, 128, 16, [127, 257], None),           # 9: the second column block holds one head
+    (2, 20, 1, 64, 16, [40, 383], None),            # 20: two groups, the second with 4
+    (3, 8, 2, 128, 16, [500, 130, 3], 0),
+    (3, 8, 2, 64, 8, [500, 130, 0], 127),
+    (2, 16, 2, 128, 16, [900, 385], 256),
+    (2, 5, 5, 128, 512, [1500, 100], 1000),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", CASES, ids=[f"B{c[0]}H{c[1]}kv{c[2]}d{c[3]}P{c[4]}w{c[6]}" for c in CASES])
+def test_decode_matches_oracle(case):
+    need_gpu()
+    B, H, Hkv, d, P, lens, window = case
+    args = _make(B, H, Hkv, d, P, lens, seed=sum(lens) % 97)
+    scale = float(np.float32(1 / math.sqrt(d)))
+    o, lse = _run(args, scale=scale, window_left=window)
+    _check(args, o, lse, scale, window)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window", [None, 6000])
+def test_split_and_unsplit(d, window):
+    """Long sequences in a small batch, with and without a workspace, and with one that holds fewer chunks."""
+    need_gpu()
+    lens = [9000, 3, 4100]
+    B, H, Hkv, P = 3, 8, 2, 16
+    args = _make(B, H, Hkv, d, P, lens, seed=4)
+    size = fa.decode_fp8_workspace_size(B, H, Hkv, d, P, args[4].shape[1], window)
+    assert size > 0
+    for n in (None, 16, size // 2):
+        ws = None if n is None else torch.empty(n, dtype=torch.uint8, device="cuda")
+        o, lse = _run(args, scale=0.1, window_left=window, workspace=ws)
+        _check(args, o, lse, 0.1, window)
+
+
+@pytest.mark.gpu
+def test_same_bits_twice():
+    need_gpu()
+    args = _make(4, 16, 4, 128, 16, [700, 64, 1, 5000], seed=8)
+    a, b = _run(args), _run(args)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [8, 16])
+def test_growing_scores_and_scales(H):
+    """Scores that grow along the positions (the reference has to move) and V rows whose scales span
+    2^-40 to 2^40, growing and shrinking; queries from 2^-60 to 2^30."""
+    need_gpu()
+    d, P, lens = 128, 16, [1500, 700]
+    q, k, v, table, sl = I.make_paged_decode(2, H, 1, d, P, lens, seed=9)
+    k, v = k.double().numpy(), v.double().numpy()
+    for b, n in enumerate(lens):
+        for j in range(n):
+            pg, s = int(table[b, j // P]), j % P
+            k[pg, s] *= (j + 1) / n * 4
+            v[pg, s] *= 2.0 ** (40 * math.sin(j / 90.0 + b))
+    kc, kb = S.quantise_rows(k)
+    vc, vb = S.quantise_rows(v)
+    sc = np.ascontiguousarray(np.stack([np.moveaxis(kb, 1, 2), np.moveaxis(vb, 1, 2)], axis=2))
+    args = (q, torch.from_numpy(kc), torch.from_numpy(vc), torch.from_numpy(sc), table, sl)
+    o, lse = _run(args, scale=0.3)
+    _check(args, o, lse, 0.3)
+    for e in (-60, 30):
+        args = (q * 2.0 ** e, *args[1:])
+        scale = 0.3 * 2.0 ** -e
+        o, lse = _run(args, scale=scale)
+        _check(args, o, lse, scale)
+        args = (q, *args[1:])
+
+
+@pytest.mark.gpu
+def test_nan_rows_reach_the_heads_that_see_them():
+    need_gpu()
+    args = _make(2, 8, 2, 128, 16, [300, 300], seed=10)
+    q, kc, vc, sc, table, sl = args
+    clean = _run(args)
+    for which in (0, 1):
+        s2 = sc.clone()
+        s2[int(table[1, 5]), 1, which, 7] = 255       # position 87 of sequence 1, K/V head 1
+        o, lse = _run((q, kc, vc, s2, table, sl))
+        assert torch.isnan(o[1, 4:].float()).all()
+        assert torch.equal(o[0], clean[0][0]) and torch.equal(o[1, :4], clean[0][1, :4])
+        if which == 0:
+            assert torch.isnan(lse[1, 4:]).all()
+        # behind the sequence's end, or before its window, it is not seen
+        short = sl.clone()
+        short[1] = 87
+        o, lse = _run((q, kc, vc, s2, table, short))
+        assert torch.isfinite(o.float()).all() and torch.isfinite(lse).all()
+        o, _ = _run((q, kc, vc, s2, table, sl), window_left=300 - 1 - 88)
+        assert torch.isfinite(o.float()).all()
+    # a query of NaN, and one of Inf
+    for bad in (float("nan"), float("inf")):
+        q2 = q.clone()
+        q2[0, 3, 9] = bad
+        o, _ = _run((q2, kc, vc, sc, table, sl))
+        assert torch.isnan(o[0, 3].float()).all()
+        keep = torch.ones(2, 8, dtype=torch.bool)
+        keep[0, 3] = False
+        assert torch.equal(o.cpu()[keep], clean[0].cpu()[keep])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("split", [False, True])
+@pytest.mark.parametrize("what", ["page_index", "negative_page", "length", "negative_length"])
+def test_out_of_range_device_inputs(what, split):
+    need_gpu()
+    lens = [100, 5000, 80] if split else [100, 50, 80]
+    B, H, Hkv, d, P = 3, 8, 2, 64, 16
+    args = _make(B, H, Hkv, d, P, lens, seed=12)
+    table, sl = args[4].clone(), args[5].clone()
+    if what == "page_index":
+        table[1, 2] = args[1].shape[0] + 5
+    elif what == "negative_page":
+        table[1, 0] = -1
+    else:
+        sl[1] = table.shape[1] * P + 1 if what == "length" else -3
+    assert (fa.decode_fp8_workspace_size(B, H, Hkv, d, P, table.shape[1]) > 0) == split
+    fa.last_device_status()
+    o, lse = fa.decode_paged_fp8(*(t.cuda() for t in (*args[:4], table, sl)), scale=0.1)
+    rc, detail = fa.last_device_status()
+    assert rc == -9 and detail == 0x2000 | (0xD2 if "page" in what else 0xD1)
+    assert torch.all(o[1] == 0) and torch.all(torch.isneginf(lse[1]))
+    _check(args, o, lse, 0.1, skip=(1,))
+
+
+@pytest.mark.gpu
+def test_pages_before_the_window_are_not_looked_up():
+    """A cache that gives back pages behind its window leaves anything in their table entries."""
+    need_gpu()
+    args = _make(2, 8, 2, 128, 16, [700, 300], seed=13)
+    q, kc, vc, sc, table, sl = args
+    want = _run(args, window_left=100)
+    t = table.clone()
+    for b, n in enumerate((700, 300)):
+        t[b, :(n - 1 - 100) // 16] = 2 ** 30
+    got = _run((q, kc, vc, sc, t, sl), window_left=100)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.gpu
+def test_full_size_sampled_sequences():
+    """64 sequences of 512 to 8192 positions, 64 query heads on 8 K/V heads, pages handed out by cache_append's
+    own quantisation: six sequences against the oracle."""
+    need_gpu()
+    lens = I.decode_lengths(64, 512, 8192, seed=21)
+    q, k, v, table, sl = (t.cuda() for t in I.make_paged_decode(64, 64, 8, 128, 16, lens, seed=21))
+    pages = k.shape[0]
+    kc, vc = (torch.zeros(k.shape, dtype=torch.uint8, device="cuda") for _ in range(2))
+    sc = torch.zeros((pages, 8, 2, 16), dtype=torch.uint8, device="cuda")
+    ident = torch.arange(pages, dtype=torch.int32, device="cuda").view(1, pages)
+    fa.cache_append(k.view(1, pages * 16, 8, 128), v.view(1, pages * 16, 8, 128), kc, vc, ident,
+                    torch.zeros(1, dtype=torch.int32, device="cuda"), kv_scale=sc)
+    o, lse = fa.decode_paged_fp8(q, kc, vc, sc, table, sl)
+    assert fa.last_device_status()[0] == 0
+    for b in (0, 7, 21, 33, 50, 63):
+        n = (int(sl[b]) + 15) // 16
+        pg = table[b, :n].long()
+        local = torch.arange(n, dtype=torch.int32).view(1, n)
+        args = (q[b:b + 1].cpu(), kc[pg].cpu(), vc[pg].cpu(), sc[pg].cpu(), local, sl[b:b + 1].cpu())
+        _check(args, o[b:b + 1], lse[b:b + 1], 1 / math.sqrt(128))
+
+
+@pytest.mark.gpu
+def test_given_outputs_and_their_checks():
+    need_gpu()
+    args = [t.cuda() for t in _make(2, 4, 2, 64, 8, [30, 9], seed=14)]
+    want = fa.decode_paged_fp8(*args)
+    o = torch.full((2, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((2, 4), 7.0, device="cuda")
+    got = fa.decode_paged_fp8(*args, out=o, lse=lse)
+    assert got[0] is o and got[1] is lse and torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    for kw in ({"out": o.float()}, {"out": o[:1]}, {"lse": lse.t()}, {"lse": lse.cpu()}, {"out": o[..., ::2]},
+               {"workspace": torch.empty(8, dtype=torch.uint8)}, {"window_left": -1}, {"window_left": 0.5}):
+        with pytest.raises((ValueError, TypeError)):
+            fa.decode_paged_fp8(*args, **kw)
+    with pytest.raises(fa.FAError):
+        fa.decode_paged_fp8(*args, scale=-1.0)

@@ -1,0 +1,146 @@
+"""The operators around the attention run together, as a serving loop runs them.
+
+A batch of prompts of different lengths goes through norm and rotation, the
+causal forward and into the cache; then tokens are decoded one by one, each
+through norm and rotation, an append and the paged decode, the step captured
+once as a CUDA graph and replayed.
+"""
+
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import exact_io_aware_51_b200 as fa
+import oracle
+from oracle import serving as S
+from tests.helpers import TOL_BF16_REL, TOL_LSE, need_gpu, rel_err
+from tests.test_gpu_decode_fp8 import _check as check_decode
+
+B, H, HKV, D, PAGE, MAX_PAGES, ROOM = 3, 8, 2, 128, 16, 20, 320
+PROMPTS = [130, 1, 77]
+
+
+def _projection(N, seed):
+    """A packed projection [B, N, H + 2 Hkv, d] as a model hands it over."""
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn((B, N, H + 2 * HKV, D), generator=g).to(torch.bfloat16).cuda()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fp8", [True, False])
+def test_prompt_then_captured_decode_steps(fp8):
+    need_gpu()
+    g = torch.Generator().manual_seed(1)
+    wq, wk = ((1 + 0.2 * torch.randn(D, generator=g)).to(torch.bfloat16).cuda() for _ in range(2))
+    cos, sin = fa.rope_tables(ROOM, D)
+    pages = B * MAX_PAGES
+    table = torch.randperm(pages, generator=g).to(torch.int32).view(B, MAX_PAGES).cuda()
+    if fp8:
+        kc, vc = (torch.zeros((pages, PAGE, HKV, D), dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2))
+        sc = torch.zeros((pages, HKV, 2, PAGE), dtype=torch.uint8, device="cuda")
+    else:
+        kc, vc = (torch.zeros((pages, PAGE, HKV, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        sc = None
+
+    # the prompts, padded to the longest
+    N = max(PROMPTS)
+    lens = torch.tensor(PROMPTS, dtype=torch.int32, device="cuda")
+    at = torch.arange(N, dtype=torch.int32, device="cuda")[None]
+    pos = torch.where(at < lens[:, None], at, -1).to(torch.int32)
+    x = _projection(N, 2)
+    q, k, v = x.split((H, HKV, HKV), dim=2)
+    qr, kr = fa.qk_norm_rope(q, k, cos, sin, wq, wk, pos)
+    o, _ = fa.fwd(qr, kr, v.contiguous(), causal=True)
+    fa.cache_append(kr, v, kc, vc, table, torch.zeros_like(lens), kv_scale=sc, count=lens)
+    # the prompt's rows against the oracle (rows behind a prompt's end are not looked at)
+    scale = float(np.float32(1 / math.sqrt(D)))
+    ro, _ = oracle.forward(qr.float().cpu(), kr.float().cpu(), v.float().cpu(), scale, True)
+    for b, n in enumerate(PROMPTS):
+        assert rel_err(o[b, :n].cpu(), ro[b, :n]) <= TOL_BF16_REL
+
+    # one decode step on buffers of its own, captured once
+    step_x = _projection(1, 3)
+    start = lens.clone()
+
+    def step():
+        q, k, v = step_x.split((H, HKV, HKV), dim=2)
+        qr, kr = fa.qk_norm_rope(q, k, cos, sin, wq, wk, start.view(B, 1))
+        fa.cache_append(kr, v, kc, vc, table, start, kv_scale=sc)
+        start.add_(1)
+        q1 = qr.view(B, H, D)
+        if fp8:
+            return (qr, kr) + tuple(fa.decode_paged_fp8(q1, kc, vc, sc, table, start))
+        return (qr, kr) + tuple(fa.decode_paged(q1, kc, vc, table, start))
+
+    before = [kc.clone(), vc.clone(), None if sc is None else sc.clone()]
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        step()
+    torch.cuda.current_stream().wait_stream(stream)
+    kc.copy_(before[0]), vc.copy_(before[1]), start.copy_(lens)
+    if sc is not None:
+        sc.copy_(before[2])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qr1, kr1, o1, lse1 = step()
+    start.copy_(lens)
+
+    ref_k, ref_v = (t.cpu().view(torch.uint8).numpy() if fp8 else t.double().cpu().numpy() for t in (kc, vc))
+    ref_s = None if sc is None else sc.cpu().numpy()
+    for t in range(5):
+        step_x.copy_(_projection(1, 10 + t))
+        graph.replay()
+        n = lens.cpu() + t
+        ref_k, ref_v, ref_s = S.cache_append(kr1.double().cpu(), step_x[:, :, H + HKV:].double().cpu(), ref_k, ref_v,
+                                             table.cpu(), n, ref_s)
+        got_k = kc.cpu().view(torch.uint8).numpy() if fp8 else kc.double().cpu().numpy()
+        assert np.array_equal(got_k, ref_k)
+        if fp8:
+            assert np.array_equal(sc.cpu().numpy(), ref_s)
+            check_decode((qr1.view(B, H, D).cpu(), torch.from_numpy(ref_k), torch.from_numpy(ref_v),
+                          torch.from_numpy(ref_s), table.cpu(), n + 1), o1, lse1, 1 / math.sqrt(D))
+        else:
+            ro, rl = oracle.decode_paged(qr1.view(B, H, D).float().cpu(), ref_k, ref_v, table.cpu(), n + 1, scale)
+            assert rel_err(o1.cpu(), ro) <= TOL_BF16_REL
+            assert np.max(np.abs(lse1.cpu().numpy() - rl)) <= TOL_LSE
+    assert fa.last_device_status()[0] == 0
+
+    # the next part of a prompt reads the cache back
+    k2, v2 = fa.cache_read(kc, vc, table, start, ROOM, kv_scale=sc)
+    K, V = S.dequantise_cache(ref_k, ref_v, ref_s) if fp8 else (ref_k, ref_v)
+    assert torch.equal(k2.cpu(), torch.from_numpy(S.cache_read(K, table.cpu(), start.cpu(), ROOM)).to(torch.bfloat16))
+    assert torch.equal(v2.cpu(), torch.from_numpy(S.cache_read(V, table.cpu(), start.cpu(), ROOM)).to(torch.bfloat16))
+
+
+@pytest.mark.gpu
+def test_two_graphs_and_an_eager_call_do_not_share_scratch():
+    """Split decodes captured twice, replayed on two streams at once beside an eager one: each has partials of its own."""
+    need_gpu()
+    from tests.test_gpu_decode_fp8 import _make
+    a = [t.cuda() for t in _make(1, 8, 2, 128, 16, [6000], seed=41)]
+    b = [t.cuda() for t in _make(1, 8, 2, 128, 16, [5000], seed=42)]
+    assert fa.decode_fp8_workspace_size(1, 8, 2, 128, 16, a[4].shape[1]) > 0
+    want = [tuple(t.clone() for t in fa.decode_paged_fp8(*x)) for x in (a, b)]
+    graphs, outs = [], []
+    for x in (a, b):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(fa.decode_paged_fp8(*x))
+        graphs.append(gr)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        for s, gr in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                gr.replay()
+        eager = fa.decode_paged_fp8(*a, stream=streams[2])
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    for got, ref in zip((*outs, eager), (*want, want[0])):
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
