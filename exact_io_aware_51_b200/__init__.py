@@ -552,64 +552,73 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None, window=
 # --------------------------------------------------------------------------
 # Around the attention: norm and rotation of query and key heads, the paged cache
 # --------------------------------------------------------------------------
-def _launch(device, stream, call):
-    """``call(handle)`` with ``device`` current and what it allocates taken from the stream that the kernels run on
-    (so that the memory of a temporary is only handed out again behind them)."""
-    if stream is None and torch.cuda.current_device() == device.index:
-        return call(torch.cuda.current_stream().cuda_stream)
+_StrideArray = ctypes.c_longlong * 3
+
+
+def _current_handle(device):
+    """Handle of the device's current stream (torch.cuda.current_stream builds a Stream object, 2 us a call)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _elsewhere(device, stream):
+    return stream is not None or torch.cuda.current_device() != device.index
+
+
+def _reenter(device, stream, call):
+    """``call()`` with ``device`` current and, if given, ``stream``: what it allocates comes from the stream that the
+    kernels run on, so the memory of a temporary is only handed out again behind them."""
     if stream is not None and stream.device != device:
         raise ValueError("stream belongs to another device than the tensors")
     with torch.cuda.device(device):
         if stream is None:
-            return call(torch.cuda.current_stream().cuda_stream)
+            return call()
         with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+            return call()
 
 
 def _strides(t, name):
     """None for a dense [B, N, heads, d] tensor, else its (batch, position, head) strides for the C call."""
-    if t.is_contiguous():
+    if t.is_contiguous() or t.numel() == 0:
         return None
+    B, N, h, _ = t.shape
     sb, sn, sh, sd = t.stride()
-    if t.numel() == 0:
-        return None
     if sd != 1:
         raise ValueError(f"{name}: the features of a head must be contiguous")
-    B, N, h, _ = t.shape
-    s = (sb if B > 1 else 0, sn if N > 1 else 0, sh if h > 1 else 0)
-    unit = 16 // t.element_size()
-    if any(x % unit for x in s):
+    if B == 1:
+        sb = 0
+    if N == 1:
+        sn = 0
+    if h == 1:
+        sh = 0
+    if (sb | sn | sh) & (16 // t.element_size() - 1):
         raise ValueError(f"{name}: strides must be multiples of 16 bytes")
-    return (ctypes.c_longlong * 3)(*s)
+    return _StrideArray(sb, sn, sh)
 
 
-def _out_like(out, shape, dtype, device, name):
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+def _check_out(out, shape, dtype, device, name):
     if out.shape != torch.Size(shape) or out.dtype != dtype or out.device != device or not out.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
-    return out
 
 
 def _rope_check(q, k, cos, sin, q_weight, k_weight, positions):
-    if q.dim() != 4 or k.dim() != 4:
+    q_shape, k_shape, cos_shape, device, dt = q.shape, k.shape, cos.shape, q.device, q.dtype
+    if len(q_shape) != 4 or len(k_shape) != 4:
         raise ValueError("expected q [B, N, H, d] and k [B, N, Hkv, d]")
-    B, N, H, d = q.shape
-    if k.shape[0] != B or k.shape[1] != N or k.shape[3] != d:
+    B, N, H, d = q_shape
+    if k_shape[0] != B or k_shape[1] != N or k_shape[3] != d:
         raise ValueError("q and k must agree in batch, positions and head dim")
-    dtype = _dtype_code(q)
-    if k.dtype != q.dtype:
+    dtype = wdtype = _dtype_code(q)
+    if k.dtype != dt:
         raise TypeError("q and k must have one dtype")
     if cos.dtype != torch.float32 or sin.dtype != torch.float32:
         raise TypeError("cos and sin must be float32")
-    if cos.dim() != 2 or cos.shape[1] * 2 != d or sin.shape != cos.shape:
+    if len(cos_shape) != 2 or cos_shape[1] * 2 != d or sin.shape != cos_shape:
         raise ValueError("cos and sin must be [positions, d / 2] tables")
     if not (cos.is_contiguous() and sin.is_contiguous()):
         raise ValueError("cos and sin must be contiguous")
     if (q_weight is None) != (k_weight is None):
         raise ValueError("give both gains or none")
-    wdtype = dtype
-    others = [k, cos, sin]
+    same = k.device == device and cos.device == device and sin.device == device
     if q_weight is not None:
         wdtype = _dtype_code(q_weight)
         if k_weight.dtype != q_weight.dtype:
@@ -618,22 +627,21 @@ def _rope_check(q, k, cos, sin, q_weight, k_weight, positions):
             raise ValueError("q_weight and k_weight must be [d]")
         if not (q_weight.is_contiguous() and k_weight.is_contiguous()):
             raise ValueError("q_weight and k_weight must be contiguous")
-        others += [q_weight, k_weight]
+        same = same and q_weight.device == device and k_weight.device == device
     if positions is None:
-        if N > cos.shape[0] and B > 0:
+        if N > cos_shape[0] and B > 0:
             raise ValueError("the tables have fewer rows than there are positions")
     else:
         if positions.dtype != torch.int32:
             raise TypeError("positions must be int32")
         if positions.shape != (B, N) or not positions.is_contiguous():
             raise ValueError("positions must be a contiguous [B, N] tensor")
-        others.append(positions)
-    for t in others:
-        if t.device != q.device:
-            raise ValueError("all tensors must share one device")
+        same = same and positions.device == device
+    if not same:
+        raise ValueError("all tensors must share one device")
     if not q.is_cuda:
         raise ValueError("tensors must live on a CUDA device (there is no CPU path)")
-    return B, N, H, k.shape[2], d, dtype, wdtype
+    return B, N, H, k_shape[2], d, dtype, wdtype
 
 
 def _ptr(t):
@@ -660,19 +668,23 @@ def qk_norm_rope_fwd(q, k, cos, sin, q_weight=None, k_weight=None, positions=Non
     ``interleaved``: pairs (2i, 2i + 1) instead of (i, i + d / 2).
     """
     B, N, H, Hkv, d, dt, wdt = _rope_check(q, k, cos, sin, q_weight, k_weight, positions)
-    qs, ks = _strides(q, "q"), _strides(k, "k")
-
-    def call(handle):
-        qo = _out_like(q_out, (B, N, H, d), q.dtype, q.device, "q_out")
-        ko = _out_like(k_out, (B, N, Hkv, d), q.dtype, q.device, "k_out")
-        rc = lib().fa_qk_norm_rope(q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), cos.data_ptr(),
-                                   sin.data_ptr(), _ptr(positions), qo.data_ptr(), ko.data_ptr(), B, N, H, Hkv, d, qs,
-                                   ks, cos.shape[0], eps, 1 if interleaved else 0, dt, wdt, handle)
-        if rc != 0:
-            raise FAError(rc, "fa_qk_norm_rope")
-        return qo, ko
-
-    return _launch(q.device, stream, call)
+    device = q.device
+    if q_out is not None:
+        _check_out(q_out, (B, N, H, d), q.dtype, device, "q_out")
+    if k_out is not None:
+        _check_out(k_out, (B, N, Hkv, d), q.dtype, device, "k_out")
+    if _elsewhere(device, stream):
+        return _reenter(device, stream, lambda: qk_norm_rope_fwd(q, k, cos, sin, q_weight, k_weight, positions, eps,
+                                                                 interleaved, q_out, k_out))
+    qo = torch.empty_like(q, memory_format=torch.contiguous_format) if q_out is None else q_out
+    ko = torch.empty_like(k, memory_format=torch.contiguous_format) if k_out is None else k_out
+    rc = lib().fa_qk_norm_rope(q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), cos.data_ptr(),
+                               sin.data_ptr(), _ptr(positions), qo.data_ptr(), ko.data_ptr(), B, N, H, Hkv, d,
+                               _strides(q, "q"), _strides(k, "k"), cos.shape[0], eps, 1 if interleaved else 0, dt, wdt,
+                               _current_handle(device))
+    if rc != 0:
+        raise FAError(rc, "fa_qk_norm_rope")
+    return qo, ko
 
 
 def qk_norm_rope_bwd(q, k, cos, sin, dq_out, dk_out, q_weight=None, k_weight=None, positions=None, eps: float = 1e-6,
@@ -686,27 +698,28 @@ def qk_norm_rope_bwd(q, k, cos, sin, dq_out, dk_out, q_weight=None, k_weight=Non
             raise ValueError(f"{name} must have the shape, dtype and device of its output")
     if workspace is not None and (workspace.device != q.device or not workspace.is_contiguous()):
         raise ValueError("workspace must be contiguous, on the device of q")
-    st = [_strides(t, n) for t, n in ((q, "q"), (k, "k"), (dq_out, "dq_out"), (dk_out, "dk_out"))]
-
-    def call(handle):
-        dq = torch.empty((B, N, H, d), dtype=q.dtype, device=q.device)
-        dk = torch.empty((B, N, Hkv, d), dtype=q.dtype, device=q.device)
-        dwq = dwk = ws = None
-        size = 0
-        if q_weight is not None:
-            dwq, dwk = torch.empty_like(q_weight), torch.empty_like(k_weight)
-            size = int(lib().fa_qk_norm_rope_workspace_size(d))
-            ws = torch.empty(max(size, 1), dtype=torch.uint8, device=q.device) if workspace is None else workspace
-            size = ws.numel() * ws.element_size()
-        rc = lib().fa_qk_norm_rope_bwd(q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), cos.data_ptr(),
-                                       sin.data_ptr(), _ptr(positions), dq_out.data_ptr(), dk_out.data_ptr(),
-                                       dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), B, N, H, Hkv, d, *st,
-                                       cos.shape[0], eps, 1 if interleaved else 0, dt, wdt, _ptr(ws), size, handle)
-        if rc != 0:
-            raise FAError(rc, "fa_qk_norm_rope_bwd")
-        return dq, dk, dwq, dwk
-
-    return _launch(q.device, stream, call)
+    if _elsewhere(q.device, stream):
+        return _reenter(q.device, stream, lambda: qk_norm_rope_bwd(q, k, cos, sin, dq_out, dk_out, q_weight, k_weight,
+                                                                   positions, eps, interleaved, workspace))
+    dq = torch.empty_like(q, memory_format=torch.contiguous_format)
+    dk = torch.empty_like(k, memory_format=torch.contiguous_format)
+    dwq = dwk = ws = None
+    size = 0
+    if q_weight is not None:
+        dwq, dwk = torch.empty_like(q_weight), torch.empty_like(k_weight)
+        ws = workspace
+        if ws is None:
+            ws = q.new_empty(max(lib().fa_qk_norm_rope_workspace_size(d), 1), dtype=torch.uint8)
+        size = ws.numel() * ws.element_size()
+    rc = lib().fa_qk_norm_rope_bwd(q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), cos.data_ptr(),
+                                   sin.data_ptr(), _ptr(positions), dq_out.data_ptr(), dk_out.data_ptr(),
+                                   dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), B, N, H, Hkv, d,
+                                   _strides(q, "q"), _strides(k, "k"), _strides(dq_out, "dq_out"),
+                                   _strides(dk_out, "dk_out"), cos.shape[0], eps, 1 if interleaved else 0, dt, wdt,
+                                   _ptr(ws), size, _current_handle(q.device))
+    if rc != 0:
+        raise FAError(rc, "fa_qk_norm_rope_bwd")
+    return dq, dk, dwq, dwk
 
 
 def _readable(g):
@@ -748,14 +761,16 @@ _SCALES = (torch.uint8, torch.float8_e8m0fnu)
 
 
 def _cache_check(k_cache, v_cache, block_table, lengths, kv_scale, what):
-    """(fp8, num_pages, page_size, Hkv, d) of a paged cache's checked tensors."""
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+    """(fp8, num_pages, page_size, Hkv, d, B, max_pages) of a paged cache's checked tensors."""
+    shape, table_shape, dtype, device = k_cache.shape, block_table.shape, k_cache.dtype, k_cache.device
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [num_pages, page_size, Hkv, d]")
-    fp8 = k_cache.dtype in _CODES
-    if not fp8 and k_cache.dtype != torch.bfloat16 or v_cache.dtype != k_cache.dtype:
+    fp8 = dtype in _CODES
+    if not fp8 and dtype != torch.bfloat16 or v_cache.dtype != dtype:
         raise TypeError("k_cache and v_cache must both be bfloat16, or float8_e4m3fn (or its uint8 codes)")
-    num_pages, page_size, Hkv, d = k_cache.shape
-    tensors = [v_cache, block_table, lengths]
+    num_pages, page_size, Hkv, d = shape
+    dense = k_cache.is_contiguous() and v_cache.is_contiguous() and block_table.is_contiguous() and lengths.is_contiguous()
+    same = v_cache.device == device and block_table.device == device and lengths.device == device
     if fp8:
         if kv_scale is None:
             raise ValueError("an 8-bit cache needs kv_scale [num_pages, Hkv, 2, page_size]")
@@ -763,23 +778,21 @@ def _cache_check(k_cache, v_cache, block_table, lengths, kv_scale, what):
             raise TypeError("kv_scale must be uint8 (or float8_e8m0fnu)")
         if kv_scale.shape != (num_pages, Hkv, 2, page_size):
             raise ValueError("kv_scale must be [num_pages, Hkv, 2, page_size]")
-        tensors.append(kv_scale)
+        dense = dense and kv_scale.is_contiguous()
+        same = same and kv_scale.device == device
     elif kv_scale is not None:
         raise ValueError("a bfloat16 cache takes no kv_scale")
     if block_table.dtype != torch.int32 or lengths.dtype != torch.int32:
         raise TypeError(f"block_table and {what} must be int32")
-    if block_table.dim() != 2 or lengths.shape != block_table.shape[:1]:
+    if len(table_shape) != 2 or lengths.shape != table_shape[:1]:
         raise ValueError(f"block_table must be [B, max_pages] and {what} [B]")
-    if not k_cache.is_contiguous():
+    if not dense:
         raise ValueError("cache tensors must be contiguous")
-    for t in tensors:
-        if not t.is_contiguous():
-            raise ValueError("cache tensors must be contiguous")
-        if t.device != k_cache.device:
-            raise ValueError("all tensors must share one device")
+    if not same:
+        raise ValueError("all tensors must share one device")
     if not k_cache.is_cuda:
         raise ValueError("tensors must live on a CUDA device (there is no CPU path)")
-    return fp8, num_pages, page_size, Hkv, d
+    return fp8, num_pages, page_size, Hkv, d, table_shape[0], table_shape[1]
 
 
 def cache_append(k, v, k_cache, v_cache, block_table, start, kv_scale=None, count=None, stream=None):
@@ -791,48 +804,53 @@ def cache_append(k, v, k_cache, v_cache, block_table, start, kv_scale=None, coun
     (or float8_e8m0fnu), a power-of-two scale per row.  block_table [B, max_pages],
     start [B] and the optional count [B] (rows of each sequence, None: N) are int32.
     """
-    fp8, num_pages, page_size, Hkv, d = _cache_check(k_cache, v_cache, block_table, start, kv_scale, "start")
-    if k.dim() != 4 or v.shape != k.shape or k.shape[0] != block_table.shape[0] or k.shape[2:] != (Hkv, d):
+    fp8, num_pages, page_size, Hkv, d, B, max_pages = _cache_check(k_cache, v_cache, block_table, start, kv_scale, "start")
+    shape, device = k.shape, k_cache.device
+    if len(shape) != 4 or v.shape != shape or shape[0] != B or shape[2] != Hkv or shape[3] != d:
         raise ValueError("k and v must be [B, N, Hkv, d] for the cache's Hkv and d and block_table's B")
     if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
         raise TypeError("k and v must be bfloat16")
-    if k.device != k_cache.device or v.device != k_cache.device:
+    if k.device != device or v.device != device:
         raise ValueError("all tensors must share one device")
     if count is not None:
         if count.dtype != torch.int32:
             raise TypeError("count must be int32")
-        if count.shape != start.shape or not count.is_contiguous() or count.device != k_cache.device:
+        if count.shape != start.shape or not count.is_contiguous() or count.device != device:
             raise ValueError("count must be a contiguous [B] tensor on the cache's device")
-    ks, vs = _strides(k, "k"), _strides(v, "v")
-
-    def call(handle):
-        rc = lib().fa_cache_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(kv_scale),
-                                   block_table.data_ptr(), start.data_ptr(), _ptr(count), k.shape[0], k.shape[1], Hkv,
-                                   d, ks, vs, page_size, num_pages, block_table.shape[1], 1 if fp8 else 0, handle)
-        if rc != 0:
-            raise FAError(rc, "fa_cache_append")
-
-    _launch(k_cache.device, stream, call)
+    if _elsewhere(device, stream):
+        return _reenter(device, stream, lambda: cache_append(k, v, k_cache, v_cache, block_table, start, kv_scale, count))
+    rc = lib().fa_cache_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(kv_scale),
+                               block_table.data_ptr(), start.data_ptr(), _ptr(count), B, shape[1], Hkv, d,
+                               _strides(k, "k"), _strides(v, "v"), page_size, num_pages, max_pages, 1 if fp8 else 0,
+                               _current_handle(device))
+    if rc != 0:
+        raise FAError(rc, "fa_cache_append")
 
 
 def cache_read(k_cache, v_cache, block_table, seqlens, length: int, kv_scale=None, k_out=None, v_out=None,
                stream=None):
     """The first ``length`` positions of every sequence out of a paged cache (fa_cache_read): returns
     (k, v) [B, length, Hkv, d] bf16, zeros at and past seqlens[b].  Cache tensors as in ``cache_append``."""
-    fp8, num_pages, page_size, Hkv, d = _cache_check(k_cache, v_cache, block_table, seqlens, kv_scale, "seqlens")
-    B, N = block_table.shape[0], int(length)
-
-    def call(handle):
-        k = _out_like(k_out, (B, N, Hkv, d), torch.bfloat16, k_cache.device, "k_out")
-        v = _out_like(v_out, (B, N, Hkv, d), torch.bfloat16, k_cache.device, "v_out")
-        rc = lib().fa_cache_read(k_cache.data_ptr(), v_cache.data_ptr(), _ptr(kv_scale), block_table.data_ptr(),
-                                 seqlens.data_ptr(), k.data_ptr(), v.data_ptr(), B, N, Hkv, d, page_size, num_pages,
-                                 block_table.shape[1], 1 if fp8 else 0, handle)
-        if rc != 0:
-            raise FAError(rc, "fa_cache_read")
-        return k, v
-
-    return _launch(k_cache.device, stream, call)
+    fp8, num_pages, page_size, Hkv, d, B, max_pages = _cache_check(k_cache, v_cache, block_table, seqlens, kv_scale,
+                                                                   "seqlens")
+    N, device = int(length), k_cache.device
+    if N < 0:
+        raise ValueError("length must be >= 0")
+    if k_out is not None:
+        _check_out(k_out, (B, N, Hkv, d), torch.bfloat16, device, "k_out")
+    if v_out is not None:
+        _check_out(v_out, (B, N, Hkv, d), torch.bfloat16, device, "v_out")
+    if _elsewhere(device, stream):
+        return _reenter(device, stream, lambda: cache_read(k_cache, v_cache, block_table, seqlens, N, kv_scale, k_out,
+                                                           v_out))
+    k = k_cache.new_empty((B, N, Hkv, d), dtype=torch.bfloat16) if k_out is None else k_out
+    v = k_cache.new_empty((B, N, Hkv, d), dtype=torch.bfloat16) if v_out is None else v_out
+    rc = lib().fa_cache_read(k_cache.data_ptr(), v_cache.data_ptr(), _ptr(kv_scale), block_table.data_ptr(),
+                             seqlens.data_ptr(), k.data_ptr(), v.data_ptr(), B, N, Hkv, d, page_size, num_pages,
+                             max_pages, 1 if fp8 else 0, _current_handle(device))
+    if rc != 0:
+        raise FAError(rc, "fa_cache_read")
+    return k, v
 
 
 def decode_fp8_workspace_size(B: int, H: int, Hkv: int, d: int, page_size: int, max_pages: int,
@@ -853,37 +871,43 @@ def decode_paged_fp8(q, k_cache, v_cache, kv_scale, block_table, seqlens, scale:
     """
     if k_cache.dtype not in _CODES:
         raise TypeError("decode_paged_fp8 takes an 8-bit cache (decode_paged: bfloat16)")
-    _, num_pages, page_size, Hkv, d = _cache_check(k_cache, v_cache, block_table, seqlens, kv_scale, "seqlens")
-    if q.dim() != 3 or q.shape[0] != block_table.shape[0] or q.shape[2] != d:
+    _, num_pages, page_size, Hkv, d, B, max_pages = _cache_check(k_cache, v_cache, block_table, seqlens, kv_scale,
+                                                                 "seqlens")
+    shape, device = q.shape, q.device
+    if len(shape) != 3 or shape[0] != B or shape[2] != d:
         raise ValueError("q must be [B, H, d] for block_table's B and the cache's d")
     if q.dtype != torch.bfloat16:
         raise TypeError("q must be bfloat16")
-    if q.device != k_cache.device or not q.is_contiguous():
+    if device != k_cache.device or not q.is_contiguous():
         raise ValueError("q must be contiguous, on the cache's device")
-    if window_left is not None and (int(window_left) != window_left or window_left < 0):
-        raise ValueError("window_left must be None or an integer >= 0")
-    if workspace is not None and (workspace.device != q.device or not workspace.is_contiguous()):
+    H, w = shape[1], -1
+    if window_left is not None:
+        w = int(window_left)
+        if w != window_left or w < 0:
+            raise ValueError("window_left must be None or an integer >= 0")
+        w = min(w, 1 << 30)
+    if out is not None:
+        _check_out(out, (B, H, d), torch.bfloat16, device, "out")
+    if lse is not None:
+        _check_out(lse, (B, H), torch.float32, device, "lse")
+    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
         raise ValueError("workspace must be contiguous, on the device of q")
-    B, H = q.shape[0], q.shape[1]
-    max_pages = block_table.shape[1]
-    w = -1 if window_left is None else min(int(window_left), 1 << 30)
-
-    def call(handle):
-        o = _out_like(out, (B, H, d), torch.bfloat16, q.device, "out")
-        l = _out_like(lse, (B, H), torch.float32, q.device, "lse")
-        ws, size = workspace, 0
-        if ws is None:
-            size = lib().fa_decode_fp8_workspace_size(B, H, Hkv, d, page_size, max_pages, w)
-            if size:
-                ws = torch.empty(size, dtype=torch.uint8, device=q.device)
-        else:
-            size = ws.numel() * ws.element_size()
-        rc = lib().fa_decode_paged_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kv_scale.data_ptr(),
-                                       block_table.data_ptr(), seqlens.data_ptr(), o.data_ptr(), l.data_ptr(), B, H,
-                                       Hkv, d, page_size, num_pages, max_pages, _scale(scale, d), w, _ptr(ws), size,
-                                       handle)
-        if rc != 0:
-            raise FAError(rc, "fa_decode_paged_fp8")
-        return o, l
-
-    return _launch(q.device, stream, call)
+    if _elsewhere(device, stream):
+        return _reenter(device, stream, lambda: decode_paged_fp8(q, k_cache, v_cache, kv_scale, block_table, seqlens,
+                                                                 scale, window_left, out, lse, workspace))
+    o = torch.empty_like(q) if out is None else out
+    l = q.new_empty((B, H), dtype=torch.float32) if lse is None else lse
+    ws = workspace
+    if ws is None:
+        size = lib().fa_decode_fp8_workspace_size(B, H, Hkv, d, page_size, max_pages, w)
+        if size:
+            ws = q.new_empty(size, dtype=torch.uint8)
+    else:
+        size = ws.numel() * ws.element_size()
+    rc = lib().fa_decode_paged_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kv_scale.data_ptr(),
+                                   block_table.data_ptr(), seqlens.data_ptr(), o.data_ptr(), l.data_ptr(), B, H, Hkv, d,
+                                   page_size, num_pages, max_pages, _scale(scale, d), w, _ptr(ws), size,
+                                   _current_handle(device))
+    if rc != 0:
+        raise FAError(rc, "fa_decode_paged_fp8")
+    return o, l

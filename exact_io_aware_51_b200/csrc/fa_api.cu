@@ -1075,7 +1075,7 @@ int fa_cache_read(const void* K_cache, const void* V_cache, const void* kv_scale
 namespace {
 
 struct Decode8Plan {
-  int nt, hgroups, splits, chunk;
+  int nt, hgroups, ranges;
   size_t ws;
 };
 
@@ -1084,13 +1084,28 @@ int check_decode8(int B, int H, int Hkv, int d, int page_size, int num_pages, in
   if (rc) return rc;
   if (window < -1) return FA_ERR_INVALID_ARG;
   if (static_cast<long long>(max_pages) * page_size > (1LL << 30)) return FA_ERR_TOO_LARGE;
-  if (static_cast<long long>(B) * H > 0x7fffffffLL) return FA_ERR_TOO_LARGE;
+  // the kernel counts the tiles of all sequences in an int
+  if (static_cast<long long>(B) * ((static_cast<long long>(max_pages) * page_size + 127) / 128) > (1LL << 30))
+    return FA_ERR_TOO_LARGE;
   return FA_OK;
 }
 
-// Chunks of positions per (sequence, head group), in tiles of 128.
+// A lone CTA takes 1.2 us for a tile; cutting a list into ranges and joining them costs 3 us
+// more than one CTA per sequence (measured, one sequence, 8 K/V heads, d = 128: 3 tiles
+// 7.1 us whole and 7.6 in ranges of one tile, 4 tiles 8.3 and 7.7, 16 tiles 23 and 8.6).
+constexpr int kDecode8WholeTiles = 3;
+
+size_t decode8_ws_bytes(int H, int d, int ranges) {
+  const size_t rows = static_cast<size_t>(ranges) * 2 * H;
+  return align256(rows * d * sizeof(float)) + align256(rows * sizeof(float)) + align256(ranges * sizeof(int4));
+}
+
+// How the tiles (128 positions) of all sequences are shared out.  Where no table row
+// holds more than kDecode8WholeTiles, or the workspace holds no two ranges, one CTA takes
+// one sequence of one head group.  Else as many ranges as CTAs fit on the GPU beside one
+// another.
 Decode8Plan decode8_plan(int B, int H, int Hkv, int d, int page_size, int max_pages, int window, size_t ws_cap) {
-  Decode8Plan p;
+  Decode8Plan p = {};
   const int G = H / Hkv;
   p.nt = G <= 8 ? 1 : 2;
   p.hgroups = (G + 8 * p.nt - 1) / (8 * p.nt);
@@ -1098,20 +1113,15 @@ Decode8Plan decode8_plan(int B, int H, int Hkv, int d, int page_size, int max_pa
   // a window's first position lies anywhere in its first tile
   if (window >= 0) span = std::min(span, static_cast<long long>(window) + 1 + 127);
   const long long tiles = (span + 127) / 128;
-  const long long ctas = static_cast<long long>(B) * Hkv * p.hgroups;
-  const long long slots = 2 * 148;
-  const long long min_tiles = d == 128 ? 8 : 16;
-  const long long w = ctas < slots ? 2 : 4;
-  long long want = ctas <= 0 ? 1 : (w * slots + ctas - 1) / ctas;
-  want = std::max(1LL, std::min({want, tiles / min_tiles, 65535LL}));
-  for (;;) {
-    const long long chunk_tiles = (tiles + want - 1) / want;
-    p.splits = static_cast<int>((tiles + chunk_tiles - 1) / chunk_tiles);
-    p.chunk = static_cast<int>(chunk_tiles * 128);
-    p.ws = decode_ws_bytes(B, H, d, p.splits);
-    if (p.splits == 1 || p.ws <= ws_cap) break;
-    want = p.splits - 1;
-  }
+  const long long slots = 148LL * fa::decode_fp8_ctas_per_sm(p.nt);
+  const long long per_range = static_cast<long long>(Hkv) * p.hgroups;
+  if (tiles <= kDecode8WholeTiles || B == 0) return p;
+  long long want = std::max(1LL, slots / per_range);
+  want = std::min({want, tiles * B, 65535LL});
+  while (want > 1 && decode8_ws_bytes(H, d, static_cast<int>(want)) > ws_cap) --want;
+  if (want < 2) return p;
+  p.ranges = static_cast<int>(want);
+  p.ws = decode8_ws_bytes(H, d, p.ranges);
   return p;
 }
 
@@ -1149,8 +1159,7 @@ int fa_decode_paged_fp8(const void* Q, const void* K_cache, const void* V_cache,
   a.num_pages = num_pages;
   a.max_pages = max_pages;
   a.hgroups = plan.hgroups;
-  a.splits = plan.splits;
-  a.chunk = plan.chunk;
+  a.ranges = plan.ranges;
   a.window = window_left;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.Q = Q;
@@ -1159,10 +1168,14 @@ int fa_decode_paged_fp8(const void* Q, const void* K_cache, const void* V_cache,
   a.seqlens = seqlens;
   a.O = O;
   a.LSE = LSE;
-  const size_t rows = static_cast<size_t>(plan.splits) * B * H;
-  a.Opart = plan.splits > 1 ? static_cast<float*>(workspace) : nullptr;
-  a.LSEpart = plan.splits > 1 ? reinterpret_cast<float*>(static_cast<char*>(workspace) + align256(rows * d * 4))
-                              : nullptr;
+  if (plan.ranges) {
+    const size_t rows = static_cast<size_t>(plan.ranges) * 2 * H;
+    char* ws = static_cast<char*>(workspace);
+    a.Opart = reinterpret_cast<float*>(ws);
+    ws += align256(rows * d * sizeof(float));
+    a.LSEpart = reinterpret_cast<float*>(ws);
+    a.borders = reinterpret_cast<int4*>(ws + align256(rows * sizeof(float)));
+  }
   CUtensorMap tk, tv;
   CUresult r;
   if ((r = make_paged_map_u8(&tk, K_cache, num_pages, page_size, Hkv, d)) != CUDA_SUCCESS ||

@@ -8,28 +8,30 @@
 //
 // Bound by the codes' bytes: each K/V row is read once per (sequence, K/V head)
 // and serves H / Hkv query heads.  What the kernel is built around:
-//   * grid (K/V head x head group, sequence, chunk of positions); the lanes of a
-//     producer warp issue one TMA box per page and tensor and one bulk copy of
-//     the page's scale bytes, 128 positions a stage, completion on mbarriers;
-//   * four consumer warps take 32 positions of a tile each, on warp-level MMAs
-//     (m16n8k16, f16 in, fp32 sums) with the POSITIONS as the 16 rows of S^T = K
-//     Q^T and the features as the rows of O^T = V^T P^T, so that up to 8 query
-//     heads fill the 8 columns and none of the tensor work is padding at H / Hkv
-//     = 8 (the heads as rows would leave half of it empty);
-//   * e4m3 -> f16 in integer arithmetic: the sign moves to bit 15 and the 7 other
-//     bits to 13..7, which is code * 2^-8 exactly, subnormals included, and is
-//     finite for every byte.  So what lies behind a sequence's end in a page can
-//     be multiplied by a zero probability as it is;
-//   * a 32-bit word of four codes gives the f16 pairs (0, 2) and (1, 3).  Along
-//     the features of K any order will do, Q is loaded in the same one: a lane
-//     reads 16 codes of a row at once.  For V, ldmatrix.trans on pairs of
-//     features hands a lane the codes (f, j), (f + 1, j), (f, j + 1), (f + 1, j +
-//     1), so the same two pairs are rows f and f + 1 of V^T: 8-bit data is
-//     transposed by the 16-bit instruction;
+//   * all tiles (128 positions) of all sequences form one list, cut into as many
+//     equal ranges as the GPU holds CTAs per head group, so lengths and batch size
+//     leave no SM idle.  The CTAs of one range's K/V heads are neighbours: they walk
+//     the same pages, whose rows of different heads are neighbours in memory.  A
+//     sequence that crosses a range's border leaves fp32 partials for the join;
+//   * a producer warp looks up a tile's pages, a lane each, and issues one TMA box
+//     per page and tensor and one bulk copy of the page's scale bytes; it runs ahead
+//     over sequence borders;
+//   * four consumer warps take 32 positions of a tile each, on warp-level MMAs with
+//     the POSITIONS as the 16 rows of S^T = K Q^T and the features as the rows of O^T
+//     = V^T P^T, so that up to 8 query heads fill the 8 columns and none of the tensor
+//     work is padding at H / Hkv = 8;
+//   * S^T multiplies the codes as they are (m16n8k32, e4m3).  A bf16 query has 8
+//     significant bits, the sum of two e4m3 values of 4: q = qh + ql / 16, two MMAs
+//     with sums of their own.  Any order of the features will do, as long as it is
+//     one: a lane reads 16 codes of a row at once;
+//   * for V^T, ldmatrix.trans on pairs of features hands a lane the codes (f, j), (f +
+//     1, j), (f, j + 1), (f + 1, j + 1); swapping the middle two and converting pairs
+//     to f16 gives rows f and f + 1: 8-bit data is transposed by the 16-bit
+//     instruction, and m16n8k16 in f16 keeps P at 11 bits;
 //   * P goes from the accumulator layout to the operand layout with movmatrix.
-// Rounding: Q is scaled by a power of two per head so that its largest element
-// is in [2^8, 2^9), which is exact in f16 but for elements 2^22 below it; P times
-// the V scales is rounded to f16 (11 bits; the running maximum of the V scales'
+// Rounding: q is scaled by a power of two per head so that its largest element is in
+// [2^7, 2^8); what qh and ql leave out is under 2^-14 then, 2^-21 of the largest.
+// P times the V scales is rounded to f16 (the running maximum of the V scales'
 // exponents is taken out, like m); sums, maxima and statistics are fp32.
 //
 // A row whose scale byte is 255 (NaN) makes the heads that see it NaN.  A
@@ -37,6 +39,7 @@
 // length outside its table row or a page index outside the pool, which is
 // reported (kDevBadInput); page 0 is read in such a page's place.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "fa_internal.h"
 #include "sm100.cuh"
@@ -52,25 +55,36 @@ constexpr int kThreads = (kConsumers + 1) * 32;
 // units): p <= 2^kLazy, and P * 2^(15 - kLazy) stays inside f16.
 constexpr float kLazy = 6.f;
 constexpr int kPShift = 9;
+constexpr int kBarBytes = 192;
 
-template <int D>
+template <int D, int NT>
 struct Cfg8 {
   static constexpr int kTileBytes = kTileKeys * D;
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kStages = D == 128 ? 3 : 4;
+  static constexpr int kStages = (D == 128 ? 2 : 4) + (NT == 2 && D == 128 ? 1 : 0);
+  static constexpr int kCtas = NT == 1 ? 3 : 2;                  // per SM
+  static constexpr int kBlocks = NT == 1 ? 2 : 1;                // blocks of 16 positions that a warp takes at a time (registers)
+  static constexpr int kRounds = NT * (D / 64);                  // the merge goes through in slices of the features
+  static constexpr int kSlice = D / kRounds;
+  static constexpr int kORow = kSlice + 4;
   static constexpr int kOffScale = kStages * kStageBytes;        // [stage][256] scale bytes
-  static constexpr int kOffBar = kOffScale + kStages * 2 * kTileKeys;
-  static constexpr int kOffML = kOffBar + 128;                   // [2][4 warps][16 heads] reference, sum
-  static constexpr int kSmemBytes = kOffML + 2 * kConsumers * 16 * 4;
-  static constexpr int kORow = D + 4;
-  static_assert(kConsumers * 16 * kORow * 4 <= kOffScale, "merge buffer fits in the stages");
+  static constexpr int kOffMerge = kOffScale + kStages * 2 * kTileKeys;
+  static constexpr int kOffML = kOffMerge + kConsumers * 8 * NT * kORow * 4;  // [2][4 warps][16 heads] reference, sum
+  static constexpr int kOffBar = kOffML + 2 * kConsumers * 16 * 4;
+  static constexpr int kSmemBytes = kOffBar + kBarBytes;
+  static_assert(kCtas * (kSmemBytes + 1024) <= 227 * 1024, "CTAs per SM");
+  static_assert(kStages <= 4, "barrier block");
 };
 
 struct Bars8 {
   uint64_t full[4], empty[4];
-  int bad, abort;
+  int bad[4];   // the stage's tile has a page outside the pool
+  int abort;
+  int first_b, first_off;  // where this CTA's range begins
+  int sums[kConsumers + 1];
+  int rows[16];  // pool rows of the tile's boxes
 };
-static_assert(sizeof(Bars8) <= 128 && Cfg8<64>::kStages <= 4 && Cfg8<128>::kStages <= 4, "barrier block");
+static_assert(sizeof(Bars8) <= kBarBytes, "barrier block");
 
 __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t* r) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -105,13 +119,52 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-// codes 0, 2 and codes 1, 3 of a word as f16 pairs, each code * 2^-8
-__device__ __forceinline__ uint32_t even_codes(uint32_t w) {
-  return ((w << 7) & 0x3f803f80u) | ((w << 8) & 0x80008000u);
+// one lane of the converged warp; the compiler knows what follows to be a single thread's code
+// and issues its bulk copies without a loop over lanes (a lane per box took twice the instructions)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
-__device__ __forceinline__ uint32_t odd_codes(uint32_t w) { return ((w >> 1) & 0x3f803f80u) | (w & 0x80008000u); }
+// codes 0, 2 and codes 1, 3 of a word as f16 pairs
+__device__ __forceinline__ void f16_pairs(uint32_t w, uint32_t& even, uint32_t& odd) {
+  asm("{\n\t.reg .b32 p;\n\t.reg .b16 lo, hi;\n\t"
+      "prmt.b32 p, %2, 0, 0x3120;\n\t"
+      "mov.b32 {lo, hi}, p;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(even), "=r"(odd)
+      : "r"(w));
+}
+// codes 0, 1 and codes 2, 3
+__device__ __forceinline__ void f16_halves(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
 
 __device__ __forceinline__ void sync_consumers() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory"); }
+
+// the same, and whether any thread passes true
+__device__ __forceinline__ bool any_consumer(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(x ? 1u : 0u), "n"(kConsumers * 32)
+      : "memory");
+  return r != 0;
+}
 
 // tile row that fragment row g (0..7) stands for: with 128-byte rows, neighbouring
 // fragment rows sit 4 rows apart, so the 8 lanes of a 128-bit shared-memory phase
@@ -152,11 +205,47 @@ __device__ __forceinline__ bool wait_ring(uint64_t* bar, uint32_t parity, Bars8*
   }
 }
 
+// The visible part of a sequence: positions [lo, len), in tiles from base on.
+struct Seq {
+  int len, lo, base, tiles;
+};
+__device__ __forceinline__ Seq sequence(const Decode8Args& a, int b) {
+  Seq s;
+  s.len = a.seqlens[b];
+  if (s.len < 0 || s.len > a.max_pages * a.page_size) s.len = 0;  // max_pages * page_size <= 2^30 (host check)
+  s.lo = a.window < 0 ? 0 : max(0, s.len - 1 - a.window);
+  s.base = s.lo & ~(kTileKeys - 1);
+  s.tiles = (s.len - s.base + kTileKeys - 1) / kTileKeys;
+  return s;
+}
+
+// This CTA's walk: up to `left` tiles from tile `off` of sequence b on, sequence by sequence.
+struct Walk {
+  int b, off, left;
+  Seq s;
+  int n;  // tiles of the current segment
+  __device__ __forceinline__ bool next(const Decode8Args& a) {  // the segment at (b, off); false at the end
+    while (left > 0) {
+      s = sequence(a, b);
+      n = min(s.tiles - off, left);
+      if (n > 0) return true;
+      ++b;
+      off = 0;
+    }
+    return false;
+  }
+  __device__ __forceinline__ void done() {
+    left -= n;
+    ++b;
+    off = 0;
+  }
+};
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
     decode_fp8_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const Decode8Args a, const DevCtl ctl) {
-  using C = Cfg8<D>;
+  using C = Cfg8<D, NT>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {  // the swizzled tiles need a 1024-byte aligned base
     if (threadIdx.x == 0) atomicCAS(ctl.status, 0, kDevTimeout | 0xC4);
@@ -165,355 +254,444 @@ __global__ void __launch_bounds__(kThreads, 2)
   Bars8* bars = reinterpret_cast<Bars8*>(smem + C::kOffBar);
   const int warp = warp_id();
   const int lane = lane_id();
-  const int split = blockIdx.z;
   const int hkv = blockIdx.x / a.hgroups;
   const int hg = blockIdx.x % a.hgroups;
-  const int b = blockIdx.y;
   const int G = a.H / a.Hkv;
   const int h0 = hkv * G + hg * (8 * NT);
   const int gv = min(8 * NT, G - hg * (8 * NT));
   const int P = a.page_size;
 
-  const int L = a.seqlens[b];
-  const bool bad_len = L < 0 || L > a.max_pages * P;  // max_pages * P <= 2^30 (host check)
-  const int lo = a.window < 0 || bad_len ? 0 : max(0, L - 1 - a.window);  // first visible position
-  // positions stay below 2^30 and chunks times splits below 2^30 + 2^30 (host checks)
-  const int kbeg = (lo & ~(kTileKeys - 1)) + split * a.chunk;
-  const int kend = bad_len ? kbeg : static_cast<int>(min(static_cast<long long>(kbeg) + a.chunk, static_cast<long long>(L)));
-  const int ntiles = kend > kbeg ? (kend - kbeg + kTileKeys - 1) / kTileKeys : 0;
   if (threadIdx.x == 0) {
-    bars->bad = bad_len ? 1 : 0;
     bars->abort = 0;
-    if (bad_len) atomicCAS(ctl.status, 0, kDevBadInput | 0xD1);
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&bars->full[s], 1);
       mbar_init(&bars->empty[s], kConsumers);
     }
     fence_mbar_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
   }
-  __syncthreads();
+  // ---- where this CTA's range of tiles begins ----
+  Walk walk;
+  const int range = blockIdx.y;
+  if (a.ranges == 0) {  // one sequence per CTA
+    walk.b = range;
+    walk.off = 0;
+    walk.left = sequence(a, range).tiles;
+    __syncthreads();
+  } else {
+    const int per = (a.B + kThreads - 1) / kThreads;
+    const int b0 = min(a.B, static_cast<int>(threadIdx.x) * per), b1 = min(a.B, b0 + per);
+    int mine = 0;
+    for (int b = b0; b < b1; ++b) mine += sequence(a, b).tiles;
+    int cum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, cum, o);
+      if (lane >= o) cum += x;
+    }
+    if (lane == 31) bars->sums[warp] = cum;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int i = 0; i <= kConsumers; ++i) {
+      if (i < warp) cum += bars->sums[i];
+      total += bars->sums[i];
+    }
+    cum -= mine;  // tiles before this thread's sequences
+    const int len = max(1, (total + a.ranges - 1) / a.ranges);
+    const long long begin = static_cast<long long>(range) * len;
+    walk.left = static_cast<int>(max(0LL, min(static_cast<long long>(len), total - begin)));
+    if (begin >= cum && begin < cum + mine) {  // one thread, if the range is not empty
+      int b = b0, t = sequence(a, b).tiles;
+      while (begin >= cum + t) {
+        cum += t;
+        t = sequence(a, ++b).tiles;
+      }
+      bars->first_b = b;
+      bars->first_off = static_cast<int>(begin) - cum;
+      if (blockIdx.x == 0) a.borders[range] = make_int4(b, cum, t, len);
+    }
+    if (threadIdx.x == 0 && blockIdx.x == 0 && walk.left == 0) a.borders[range] = make_int4(-1, 0, 0, 0);
+    __syncthreads();
+    walk.b = bars->first_b;
+    walk.off = bars->first_off;
+  }
   const int R = min(P, kTileKeys);  // positions per box
 
   if (warp == kConsumers) {
-    // ===================== producer warp: lane i loads box i of a tile =====================
-    if (ntiles > 0) {
-      const int* table = a.block_table + static_cast<size_t>(b) * a.max_pages;
-      if (lane == 0) {
-        tma_prefetch_desc(&tmK);
-        tma_prefetch_desc(&tmV);
-      }
+    // ===================== producer warp: lane i looks up the page of box i of a tile =====================
+    int issued = 0;
+    bool going = true;
+    while (going && walk.next(a)) {
+      const int* table = a.block_table + static_cast<size_t>(walk.b) * a.max_pages;
+      const int kbeg = walk.s.base + walk.off * kTileKeys, kend = walk.s.len, lo = walk.s.lo;
       auto page_of = [&](int t) {  // this lane's page of tile t (nothing is read outside [lo, kend))
         const int j = kbeg + t * kTileKeys + lane * R;
         return (lane * R < kTileKeys && j < kend && j + R > lo) ? table[j / P] : 0;
       };
-      int issued = 0;
       int next = page_of(0);
-      for (int t = 0; t < ntiles; ++t) {
-        const int st = t % C::kStages;
+      for (int t = 0; t < walk.n; ++t) {
+        const int st = issued % C::kStages;
         int page = next;
-        if (t + 1 < ntiles) next = page_of(t + 1);
-        const bool free =
-            t < C::kStages || wait_ring(&bars->empty[st], ((t / C::kStages) - 1) & 1, bars, ctl, 0xC5);
-        if (!__all_sync(0xffffffffu, free)) break;
+        if (t + 1 < walk.n) next = page_of(t + 1);
+        const bool free = issued < C::kStages ||
+                          wait_ring(&bars->empty[st], ((issued / C::kStages) - 1) & 1, bars, ctl, 0xC5);
+        if (!__all_sync(0xffffffffu, free)) {
+          going = false;
+          break;
+        }
         const int key0 = kbeg + t * kTileKeys;
         const int nbox = (min(kTileKeys, kend - key0) + R - 1) / R;
         const int b0 = max(0, lo - key0) / R;  // boxes wholly before the window are left out
         const bool mine = lane >= b0 && lane < nbox;
-        if (mine && (page < 0 || page >= a.num_pages)) {
+        const bool bad = mine && (page < 0 || page >= a.num_pages);
+        if (bad) {
           atomicCAS(ctl.status, 0, kDevBadInput | 0xD2);
-          *reinterpret_cast<volatile int*>(&bars->bad) = 1;
           page = 0;
         }
-        __syncwarp();  // the flag is set before lane 0 arrives
-        if (lane == 0)
-          mbar_arrive_expect_tx(&bars->full[st], static_cast<uint32_t>((nbox - b0) * R * (2 * D + 2)));
+        const bool any_bad = __any_sync(0xffffffffu, bad);
+        if (mine) bars->rows[lane] = page * P + ((key0 + lane * R) & (P - 1));
         __syncwarp();
-        if (mine) {
-          uint8_t* ks = smem + st * C::kStageBytes + lane * R * D;
-          uint8_t* sc = smem + C::kOffScale + st * 2 * kTileKeys + lane * 2 * R;
-          const int slot = (key0 + lane * R) & (P - 1);
-          const int row = page * P + slot;
-          tma_load_2d(ks, &tmK, &bars->full[st], hkv * D, row);
-          tma_load_2d(ks + C::kTileBytes, &tmV, &bars->full[st], hkv * D, row);
-          const uint8_t* src = a.kv_scale + (static_cast<size_t>(page) * a.Hkv + hkv) * 2 * P + slot;
-          if (P <= kTileKeys) {  // the page's K bytes and V bytes are neighbours
-            bulk_load(sc, src, 2 * R, &bars->full[st]);
-          } else {
-            bulk_load(sc, src, R, &bars->full[st]);
-            bulk_load(sc + R, src + P, R, &bars->full[st]);
+        if (elect_one()) {
+          uint64_t* full = &bars->full[st];
+          bars->bad[st] = any_bad ? 1 : 0;  // before the arrival, which releases it
+          mbar_arrive_expect_tx(full, static_cast<uint32_t>((nbox - b0) * R * (2 * D + 2)));
+          uint8_t* ks = smem + st * C::kStageBytes;
+          uint8_t* sc = smem + C::kOffScale + st * 2 * kTileKeys;
+          for (int i = b0; i < nbox; ++i) {
+            const int row = bars->rows[i];
+            tma_load_2d(ks + i * R * D, &tmK, full, hkv * D, row);
+            tma_load_2d(ks + i * R * D + C::kTileBytes, &tmV, full, hkv * D, row);
+            const int slot = row & (P - 1);
+            const uint8_t* src = a.kv_scale + (static_cast<size_t>(row - slot) * a.Hkv + hkv * P) * 2 + slot;
+            if (P <= kTileKeys) {  // the page's K bytes and V bytes are neighbours
+              bulk_load(sc + i * 2 * R, src, 2 * R, full);
+            } else {
+              bulk_load(sc, src, R, full);
+              bulk_load(sc + R, src + P, R, full);
+            }
           }
         }
+        __syncwarp();  // the rows have been read
         ++issued;
       }
-      // no copy of this CTA may still be writing its shared memory when it exits
-      if (lane == 0) drain_ring(bars->full, C::kStages, issued, ctl.limit_ns);
+      walk.done();
     }
-    return;  // the consumers' merge below syncs only the four consumer warps
+    // no copy of this CTA may still be writing its shared memory when it exits
+    if (lane == 0) drain_ring(bars->full, C::kStages, issued, ctl.limit_ns);
+    return;  // the consumers' merges below sync only the four consumer warps
   }
 
   // ===================== consumers =====================
+  // sequences without a visible position, shared out over the ranges
+  for (int b = range; b < a.B; b += gridDim.y) {
+    if (sequence(a, b).tiles != 0) continue;
+    if (threadIdx.x == 0 && a.seqlens[b] != 0) atomicCAS(ctl.status, 0, kDevBadInput | 0xD1);
+    const size_t row = static_cast<size_t>(b) * a.H + h0;
+    for (int i = threadIdx.x; i < gv * D / 8; i += kConsumers * 32)
+      st_global_v4(static_cast<__nv_bfloat16*>(a.O) + row * D + i * 8, 0u, 0u, 0u, 0u);
+    for (int i = threadIdx.x; i < gv; i += kConsumers * 32) a.LSE[row + i] = -INFINITY;
+  }
+
   const int g = lane >> 2;  // fragment row (position, feature pair) and column (head)
   const int t4 = lane & 3;
   const int kg = key_of<D>(g);
-  // Q as the B operand: head nt * 8 + g, in the order in which even_codes / odd_codes
-  // hand over the 16-byte units t4 (and t4 + 4) of a K row
-  uint32_t qb[NT][D / 16][2];
-  float qf[NT][2];  // heads 2 t4, 2 t4 + 1: scale_log2 * 2^8 / (the power of two put into Q)
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const bool have = nt * 8 + g < gv;
-    const uint4* qrow =
-        reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.Q) + (static_cast<size_t>(b) * a.H + h0 + nt * 8 + (have ? g : 0)) * D);
-    uint4 raw[D / 32];
-    uint32_t mx = 0;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {  // features [16 u, 16 u + 16) of unit u = t4 + 4 (i / 2)
-      raw[i] = have ? qrow[(t4 + 4 * (i >> 1)) * 2 + (i & 1)] : make_uint4(0u, 0u, 0u, 0u);
-      constexpr uint32_t kAbs = 0x7fff7fffu;
-      mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(raw[i].x & kAbs, raw[i].y & kAbs), __vmaxu2(raw[i].z & kAbs, raw[i].w & kAbs)));
-    }
-    mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-    mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-    // exponent of the largest element; at least 9, so that 2^(135 - e) is a normal number
-    const int e = max(9, static_cast<int>(max(mx & 0xffffu, mx >> 16) >> 7));
-    const float up = __uint_as_float(static_cast<uint32_t>(262 - e) << 23);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const uint32_t wd[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {  // four features = one word of codes = one k step
-        const float f0 = __uint_as_float(wd[2 * k] << 16) * up, f1 = __uint_as_float(wd[2 * k] & 0xffff0000u) * up;
-        const float f2 = __uint_as_float(wd[2 * k + 1] << 16) * up, f3 = __uint_as_float(wd[2 * k + 1] & 0xffff0000u) * up;
-        qb[nt][2 * i + k][0] = pack_f16x2(f0, f2);
-        qb[nt][2 * i + k][1] = pack_f16x2(f1, f3);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int eh = __shfl_sync(0xffffffffu, e, (2 * t4 + i) * 4);
-      qf[nt][i] = scalbnf(a.scale_log2, 8 + eh - 135);
-    }
-  }
-
-  float o[D / 16][NT][4];
-  float m[NT][2], l[NT][2];
-#pragma unroll
-  for (int c = 0; c < D / 16; ++c)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) o[c][nt][0] = o[c][nt][1] = o[c][nt][2] = o[c][nt][3] = 0.f;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) m[nt][0] = m[nt][1] = -INFINITY, l[nt][0] = l[nt][1] = 0.f;
-  int eref = 0;  // the largest V scale byte so far: P is multiplied by 2^(byte - eref)
-
-  // this lane's four positions of a tile: u * 16 + hh * 8 + kg of its warp's 32
-  uint32_t soff[2][2];  // their K scale bytes in the stage's scale block; V's lie R further
-#pragma unroll
-  for (int u = 0; u < 2; ++u)
-#pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      const int key = warp * kWarpKeys + u * 16 + hh * 8 + kg;
-      soff[u][hh] = static_cast<uint32_t>(key / R * 2 * R + key % R);
-    }
   const int mi = lane >> 3, rr = lane & 7;
+  // lane i looks after the scales of its warp's position i
+  const int my_key = warp * kWarpKeys + lane;
+  const uint32_t my_scale = static_cast<uint32_t>(my_key / R * 2 * R + my_key % R);
+  float* mw = reinterpret_cast<float*>(smem + C::kOffML);  // [4][16]
+  float* lw = mw + kConsumers * 16;
 
-  for (int t = 0; t < ntiles; ++t) {
-    const int st = t % C::kStages;
-    if (!__all_sync(0xffffffffu, wait_ring(&bars->full[st], (t / C::kStages) & 1, bars, ctl, 0xC6))) break;
-    const int key0 = kbeg + t * kTileKeys;
-    const uint32_t ks = smem_u32(smem + st * C::kStageBytes) + warp * kWarpKeys * D;
-    const uint32_t vs = ks + C::kTileBytes;
-    const uint32_t sc = smem_u32(smem + C::kOffScale + st * 2 * kTileKeys);
-
-    // S^T = K Q^T
-    float s[2][NT][4];
+  int it = 0;  // tiles so far
+  while (walk.next(a)) {
+    const int kend = walk.s.len, lo = walk.s.lo;
+    const int kbeg = walk.s.base + walk.off * kTileKeys;
+    // Q as the B operand: head nt * 8 + g, the features in the order in which a lane holds a K row
+    // (its 16-byte units t4 and, for d = 128, t4 + 4): q = (qh + ql / 16) 2^(e - 134)
+    uint32_t qb[NT][D / 16][2];
+    float qf[NT][2];  // heads 2 t4, 2 t4 + 1: scale_log2 * 2^(e - 134)
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool have = nt * 8 + g < gv;
+      const uint4* qrow = reinterpret_cast<const uint4*>(
+          static_cast<const __nv_bfloat16*>(a.Q) +
+          (static_cast<size_t>(walk.b) * a.H + h0 + (have ? nt * 8 + g : 0)) * D);
+      uint4 raw[D / 32];
+      uint32_t mx = 0;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.f;
+      for (int i = 0; i < D / 32; ++i) {  // half i % 2 (8 features) of unit t4 + 4 (i / 2)
+        raw[i] = have ? qrow[(t4 + 4 * (i >> 1)) * 2 + (i & 1)] : make_uint4(0u, 0u, 0u, 0u);
+        constexpr uint32_t kAbs = 0x7fff7fffu;
+        mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(raw[i].x & kAbs, raw[i].y & kAbs), __vmaxu2(raw[i].z & kAbs, raw[i].w & kAbs)));
+      }
+      mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = __vmaxu2(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      // exponent of the largest element; at least 9, so that 2^(134 - e) is a normal number
+      const int e = max(9, static_cast<int>(max(mx & 0xffffu, mx >> 16) >> 7));
+      const float up = e == 255 ? __uint_as_float(0x7fc00000u) : __uint_as_float(static_cast<uint32_t>(261 - e) << 23);
 #pragma unroll
-      for (int q = 0; q < D / 64; ++q) {
-        const uint4 ra = lds128(ks + unit_off<D>(u * 16 + kg, t4 + 4 * q));
-        const uint4 rb = lds128(ks + unit_off<D>(u * 16 + 8 + kg, t4 + 4 * q));
-        const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+      for (int i = 0; i < D / 32; ++i) {
+        const uint32_t wd[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t a0 = even_codes(wa[k]), a1 = even_codes(wb[k]), a2 = odd_codes(wa[k]), a3 = odd_codes(wb[k]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16(s[u][nt], a0, a1, a2, a3, qb[nt][4 * q + k][0], qb[nt][4 * q + k][1]);
+        for (int k = 0; k < 2; ++k) {  // four features = one word of codes
+          qb[nt][2 * i + k][0] = pack_f16x2(__uint_as_float(wd[2 * k] << 16) * up, __uint_as_float(wd[2 * k] & 0xffff0000u) * up);
+          qb[nt][2 * i + k][1] =
+              pack_f16x2(__uint_as_float(wd[2 * k + 1] << 16) * up, __uint_as_float(wd[2 * k + 1] & 0xffff0000u) * up);
         }
       }
-    }
-    // scores in log2 units; positions outside [lo, kend) are hidden, whatever their bytes are
-    const bool edge = key0 + kTileKeys > kend || key0 < lo;
-    float kf[2][2];
-    uint32_t vb[2][2];
-    uint32_t hidden = 0;
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        kf[u][hh] = scale_of(lds_u8(sc + soff[u][hh]));
-        vb[u][hh] = lds_u8(sc + soff[u][hh] + R);
-        if (edge) {
-          const int key = key0 + warp * kWarpKeys + u * 16 + hh * 8 + kg;
-          if (key >= kend || key < lo) {
-            hidden |= 1u << (2 * u + hh);
-            vb[u][hh] = 0;
-          }
-        }
-      }
-    float mx[NT][2];
-    bool grow = false;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float v = -INFINITY;
+        const int eh = __shfl_sync(0xffffffffu, e, (2 * t4 + i) * 4);
+        // kept finite and positive, so that a hidden score stays -inf
+        qf[nt][i] = fminf(fmaxf(scalbnf(a.scale_log2, eh - 134), 1.2e-38f), 3e38f);
+      }
+    }
+    // scores are held as t = <q, k> with q's power of two still in it: x = t qf
+    float o[D / 16][NT][4];
+    float mt[NT][2], mq[NT][2], lazy[NT][2];  // reference in t; mq = reference in x (0 while there is none)
+    float2 l[NT];
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+    for (int c = 0; c < D / 16; ++c)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) o[c][nt][0] = o[c][nt][1] = o[c][nt][2] = o[c][nt][3] = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      l[nt] = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        mt[nt][i] = -INFINITY;
+        mq[nt][i] = 0.f;
+        lazy[nt][i] = fminf(kLazy / qf[nt][i], 1e30f);
+      }
+    }
+    int eref = 0;  // the largest V scale byte so far: P is multiplied by 2^(byte - eref)
+    int bad = 0;
+
+    bool ok = true;
+    for (int t = 0; t < walk.n; ++t, ++it) {
+      const int st = it % C::kStages;
+      if (!__all_sync(0xffffffffu, wait_ring(&bars->full[st], (it / C::kStages) & 1, bars, ctl, 0xC6))) {
+        ok = false;
+        break;
+      }
+      const int key0 = kbeg + t * kTileKeys;
+      const uint32_t ks = smem_u32(smem + st * C::kStageBytes) + warp * kWarpKeys * D;
+      const uint32_t vs = ks + C::kTileBytes;
+      const uint32_t sc = smem_u32(smem + C::kOffScale + st * 2 * kTileKeys) + my_scale;
+      bad |= *reinterpret_cast<volatile int*>(&bars->bad[st]);
+
+      // this lane's position: factor of K, byte of V
+      const float kf = scale_of(lds_u8(sc));
+      int vbyte = static_cast<int>(lds_u8(sc + R));
+
+      // positions outside [lo, kend) are hidden, whatever their bytes are; their V rows are
+      // zeroed, because 0 * NaN would reach the sums
+      const bool edge = key0 + kTileKeys > kend || key0 < lo;
+      if (edge) {
+        const int first = key0 + warp * kWarpKeys;
+        if (first + lane >= kend || first + lane < lo) vbyte = 0;
+        for (int i = lane; i < kWarpKeys * (D / 16); i += 32) {
+          const int r = i / (D / 16);
+          if (first + r >= kend || first + r < lo) st_shared_v4(vs + unit_off<D>(r, i % (D / 16)), 0u, 0u, 0u, 0u);
+        }
+        __syncwarp();
+      }
+#pragma unroll 1
+      for (int u0 = 0; u0 < 2; u0 += C::kBlocks) {
+      // S^T = K Q^T
+      float s[C::kBlocks][NT][4];
+#pragma unroll
+      for (int u = 0; u < C::kBlocks; ++u) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.f;
+#pragma unroll
+        for (int q = 0; q < D / 64; ++q) {
+          const uint4 ra = lds128(ks + unit_off<D>((u0 + u) * 16 + kg, t4 + 4 * q));
+          const uint4 rb = lds128(ks + unit_off<D>((u0 + u) * 16 + 8 + kg, t4 + 4 * q));
+          const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t a0, a1, a2, a3;
+            f16_halves(wa[k], a0, a2);
+            f16_halves(wb[k], a1, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(s[u][nt], a0, a1, a2, a3, qb[nt][4 * q + k][0], qb[nt][4 * q + k][1]);
+          }
+        }
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const float f = __shfl_sync(0xffffffffu, kf, (u0 + u) * 16 + hh * 8 + kg);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) s[u][nt][2 * hh + i] *= f;
+        }
+      }
+      if (edge) {
+#pragma unroll
+        for (int u = 0; u < C::kBlocks; ++u)
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
-            float& x = s[u][nt][2 * hh + i];
-            x = (x * kf[u][hh]) * qf[nt][i];
-            if (hidden >> (2 * u + hh) & 1u) x = -INFINITY;
-            v = fmaxf(v, x);
+            const int key = key0 + warp * kWarpKeys + (u0 + u) * 16 + hh * 8 + kg;
+            if (key >= kend || key < lo) {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) s[u][nt][2 * hh] = s[u][nt][2 * hh + 1] = -INFINITY;
+            }
           }
-        mx[nt][i] = v;
-        grow |= v > m[nt][i] + kLazy;
       }
-    const uint32_t bmax = max(max(vb[0][0], vb[0][1]), max(vb[1][0], vb[1][1]));
-    if (__any_sync(0xffffffffu, grow || static_cast<int>(bmax) > eref)) {
-      const int en = max(eref, static_cast<int>(__reduce_max_sync(0xffffffffu, bmax)));
-      const float eal = __uint_as_float(static_cast<uint32_t>(max(0, 127 + eref - en)) << 23);
-      eref = en;
+      float mx[NT][2];
+      bool grow = vbyte > eref;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          float v = mx[nt][i];
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-          v = fmaxf(v, m[nt][i]);
-          const float al = (v == -INFINITY) ? 1.f : ex2(m[nt][i] - v);
-          m[nt][i] = v;
-          l[nt][i] *= al;
-          const float oal = al * eal;
+          mx[nt][i] = fmaxf(s[0][nt][i], s[0][nt][2 + i]);
+          if constexpr (C::kBlocks == 2) mx[nt][i] = fmaxf(mx[nt][i], fmaxf(s[1][nt][i], s[1][nt][2 + i]));
+          grow |= mx[nt][i] > mt[nt][i] + lazy[nt][i];
+        }
+      if (__any_sync(0xffffffffu, grow)) {
+        const int en = max(eref, static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<uint32_t>(vbyte))));
+        const float eal = __uint_as_float(static_cast<uint32_t>(max(0, 127 + eref - en)) << 23);
+        eref = en;
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            o[c][nt][i] *= oal;
-            o[c][nt][2 + i] *= oal;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float v = mx[nt][i];
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            v = fmaxf(v, mt[nt][i]);
+            const float al = (v == -INFINITY) ? 1.f : ex2((mt[nt][i] - v) * qf[nt][i]);
+            mt[nt][i] = v;
+            mq[nt][i] = (v == -INFINITY) ? 0.f : v * qf[nt][i];
+            if (i == 0) l[nt].x *= al;
+            else l[nt].y *= al;
+            const float oal = al * eal;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              o[c][nt][i] *= oal;
+              o[c][nt][2 + i] *= oal;
+            }
+          }
+      }
+      // P^T as the B operand: p * 2^(V byte - eref) * 2^kPShift in f16, transposed
+      const float vf = __uint_as_float(static_cast<uint32_t>(max(0, vbyte - eref + 127 + kPShift)) << 23);
+      uint32_t pb[C::kBlocks][NT][2];
+#pragma unroll
+      for (int u = 0; u < C::kBlocks; ++u)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          const float f = __shfl_sync(0xffffffffu, vf, (u0 + u) * 16 + hh * 8 + kg);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float2 p = make_float2(ex2(fmaf(s[u][nt][2 * hh], qf[nt][0], -mq[nt][0])),
+                                         ex2(fmaf(s[u][nt][2 * hh + 1], qf[nt][1], -mq[nt][1])));
+            l[nt] = fadd2(l[nt], p);
+            const float2 pv = fmul2(p, make_float2(f, f));
+            pb[u][nt][hh] = movmatrix_t(pack_f16x2(pv.x, pv.y));
           }
         }
+      // O^T += V^T P^T: one ldmatrix.trans covers 16 positions x 32 features
+#pragma unroll
+      for (int u = 0; u < C::kBlocks; ++u)
+#pragma unroll
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t r[4];
+          ldsm_x4_t(vs + unit_off<D>((u0 + u) * 16 + (mi & 1) * 8 + key_of<D>(rr), 2 * cc + (mi >> 1)), r);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t a0, a1, a2, a3;
+            f16_pairs(r[2 * i], a0, a1);
+            f16_pairs(r[2 * i + 1], a2, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(o[2 * cc + i][nt], a0, a1, a2, a3, pb[u][nt][0], pb[u][nt][1]);
+          }
+        }
+      }
+      if (edge) fence_proxy_async_smem();  // the next TMA write of the stage follows the zeros
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->empty[st]);
     }
-    // P^T as the B operand: p * 2^(V byte - eref) * 2^kPShift in f16, transposed
-    uint32_t pb[2][NT][2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const uint32_t vbyte = vb[u][hh];
-        const float vf = vbyte == 255u
-                             ? __uint_as_float(0x7fc00000u)
-                             : __uint_as_float(static_cast<uint32_t>(max(0, static_cast<int>(vbyte) - eref + 127 + kPShift)) << 23);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-          const float b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-          const float p0 = ex2(s[u][nt][2 * hh] - b0), p1 = ex2(s[u][nt][2 * hh + 1] - b1);
-          l[nt][0] += p0;
-          l[nt][1] += p1;
-          pb[u][nt][hh] = movmatrix_t(pack_f16x2(p0 * vf, p1 * vf));
-        }
-      }
-    // O^T += V^T P^T: one ldmatrix.trans covers 16 positions x 32 features
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int cc = 0; cc < D / 32; ++cc) {
-        uint32_t r[4];
-        ldsm_x4_t(vs + unit_off<D>(u * 16 + (mi & 1) * 8 + key_of<D>(rr), 2 * cc + (mi >> 1)), r);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t a0 = even_codes(r[2 * i]), a1 = odd_codes(r[2 * i]);
-          const uint32_t a2 = even_codes(r[2 * i + 1]), a3 = odd_codes(r[2 * i + 1]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16(o[2 * cc + i][nt], a0, a1, a2, a3, pb[u][nt][0], pb[u][nt][1]);
-        }
-      }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bars->empty[st]);
-  }
 
-  // ---- merge the four warps ----
-  float* mw = reinterpret_cast<float*>(smem + C::kOffML);  // [4][16]
-  float* lw = mw + kConsumers * 16;
+    // ---- merge the four warps ----
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float v = l[nt][i];
-      v += __shfl_xor_sync(0xffffffffu, v, 4);
-      v += __shfl_xor_sync(0xffffffffu, v, 8);
-      v += __shfl_xor_sync(0xffffffffu, v, 16);
-      if (g == 0) {
-        mw[warp * 16 + nt * 8 + 2 * t4 + i] = m[nt][i];
-        lw[warp * 16 + nt * 8 + 2 * t4 + i] = v;
+      for (int i = 0; i < 2; ++i) {
+        float v = i == 0 ? l[nt].x : l[nt].y;
+        v += __shfl_xor_sync(0xffffffffu, v, 4);
+        v += __shfl_xor_sync(0xffffffffu, v, 8);
+        v += __shfl_xor_sync(0xffffffffu, v, 16);
+        if (g == 0) {
+          mw[warp * 16 + nt * 8 + 2 * t4 + i] = mt[nt][i] == -INFINITY ? -INFINITY : mq[nt][i];
+          lw[warp * 16 + nt * 8 + 2 * t4 + i] = v;
+        }
       }
+    sync_consumers();
+    auto head_max = [&](int h) {
+      float v = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kConsumers; ++i) v = fmaxf(v, mw[i * 16 + h]);
+      return v;
+    };
+    float of[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        // P's 2^kPShift and the V exponent go out here.  A warp that saw nothing has zeros (or
+        // NaN, if all it saw was NaN) and takes them as they are.
+        const float f = scalbnf(ex2(mq[nt][i] - head_max(nt * 8 + 2 * t4 + i)), eref - 127 - kPShift);
+        of[nt][i] = eref == 255 ? __uint_as_float(0x7fc00000u) : mt[nt][i] == -INFINITY ? 1.f : f;
+      }
+    // head and features of this thread in every slice
+    constexpr int kPer = C::kSlice * 8 * NT / (kConsumers * 32);
+    const int h = threadIdx.x / (C::kSlice / kPer);
+    const int c0 = threadIdx.x % (C::kSlice / kPer) * kPer;
+    const float M = head_max(h);
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < kConsumers; ++i) {
+      const float x = mw[i * 16 + h];
+      sum += lw[i * 16 + h] * (x == -INFINITY ? 1.f : ex2(x - M));
     }
-  sync_consumers();  // the statistics are written, and every warp is done reading the stages
-  auto head_max = [&](int h) {
-    float v = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < kConsumers; ++i) v = fmaxf(v, mw[i * 16 + h]);
-    return v;
-  };
-  float* ob = reinterpret_cast<float*>(smem) + warp * 8 * NT * C::kORow;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int h = nt * 8 + 2 * t4 + i;
-      const float M = head_max(h);
-      // the codes' 2^-8, P's 2^kPShift and the V exponent go out here.  A warp that saw
-      // nothing has zeros (or NaN, if all it saw was NaN) and takes them as they are.
-      const float f = m[nt][i] == -INFINITY ? 1.f : scalbnf(ex2(m[nt][i] - M), eref - 127 + 8 - kPShift);
-#pragma unroll
-      for (int c = 0; c < D / 16; ++c)
-        *reinterpret_cast<float2*>(ob + h * C::kORow + 16 * c + 2 * g) = make_float2(o[c][nt][i] * f, o[c][nt][2 + i] * f);
+    const bool none = bad || sum == 0.f;
+    const float inv = none ? 0.f : 1.f / sum;
+    const bool whole = walk.n == walk.s.tiles;
+    const size_t row = static_cast<size_t>(walk.b) * a.H + h0 + h;
+    // a partial's slot: the range's first (the sequence began earlier) or second one
+    const size_t part = (static_cast<size_t>(range) * 2 + (walk.off == 0 ? 1 : 0)) * a.H + h0 + h;
+    if (h < gv && c0 == 0) {
+      const float lse = none ? -INFINITY : (M == -INFINITY ? sum : (M + __log2f(sum)) * 0.69314718055994531f);
+      if (whole) a.LSE[row] = lse;
+      else a.LSEpart[part] = bad ? INFINITY : lse;  // +inf never comes out of a sum: the sequence is not to be used
     }
-  sync_consumers();
-  {
-    constexpr int kPer = D * 8 * NT / (kConsumers * 32);  // features per thread
-    const int h = threadIdx.x / (D / kPer);
-    const int c0 = threadIdx.x % (D / kPer) * kPer;
-    if (h < gv) {
-      const float M = head_max(h);
-      float sum = 0.f;
+    float* ob = reinterpret_cast<float*>(smem + C::kOffMerge);
 #pragma unroll
-      for (int i = 0; i < kConsumers; ++i) {
-        const float mi_ = mw[i * 16 + h];
-        sum += lw[i * 16 + h] * (mi_ == -INFINITY ? 1.f : ex2(mi_ - M));
-      }
-      const bool bad = bars->bad != 0;
-      const bool none = bad || sum == 0.f;
-      const float inv = none ? 0.f : 1.f / sum;
-      const int hq = h0 + h;
-      const size_t ri = (static_cast<size_t>(split) * a.B + b) * a.H + hq;
-      if (threadIdx.x % (D / kPer) == 0) {
-        const float lse = none ? -INFINITY : (M == -INFINITY ? sum : (M + __log2f(sum)) * 0.69314718055994531f);
-        if (a.splits == 1) a.LSE[static_cast<size_t>(b) * a.H + hq] = lse;
-        else a.LSEpart[ri] = bad ? INFINITY : lse;  // +inf never comes out of a sum: the chunk is not to be used
-      }
-      if (a.splits == 1 || !none) {
+    for (int rd = 0; rd < C::kRounds; ++rd) {
+      if (rd) sync_consumers();  // the slice before has been read
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int c = 0; c < C::kSlice / 16; ++c) {
+            const float* x = o[rd * (C::kSlice / 16) + c][nt];
+            *reinterpret_cast<float2*>(ob + (warp * 8 * NT + nt * 8 + 2 * t4 + i) * C::kORow + 16 * c + 2 * g) =
+                make_float2(x[i] * of[nt][i], x[2 + i] * of[nt][i]);
+          }
+      sync_consumers();
+      if (h < gv) {
 #pragma unroll
         for (int c = 0; c < kPer; c += 4) {
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
           if (!none) {
 #pragma unroll
             for (int i = 0; i < kConsumers; ++i) {
-              const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem) +
-                                                                (i * 8 * NT + h) * C::kORow + c0 + c);
+              const float4 x = *reinterpret_cast<const float4*>(ob + (i * 8 * NT + h) * C::kORow + c0 + c);
               v.x += x.x;
               v.y += x.y;
               v.z += x.z;
@@ -524,33 +702,45 @@ __global__ void __launch_bounds__(kThreads, 2)
             v.z *= inv;
             v.w *= inv;
           }
-          if (a.splits == 1) {
-            __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.O) + (static_cast<size_t>(b) * a.H + hq) * D + c0 + c;
-            *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-          } else {
-            *reinterpret_cast<float4*>(a.Opart + ri * D + c0 + c) = v;
+          const int f = rd * C::kSlice + c0 + c;
+          if (whole) {
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + row * D + f) =
+                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+          } else if (!none) {
+            *reinterpret_cast<float4*>(a.Opart + part * D + f) = v;
           }
         }
       }
     }
+    // statistics and slice have been read: the next segment may write its own, unless a wait gave up
+    if (any_consumer(!ok)) break;
+    walk.done();
   }
 }
 
-// Joins the chunks of one (sequence, query head): four warps take every fourth
-// chunk.  With M = max LSE_s and w_s = exp(LSE_s - M), O = sum w_s O_s / sum w_s and
-// LSE = M + ln sum w_s.  A chunk without positions (-inf) has no partial output; a
-// chunk that is not to be used (+inf) makes the row empty.
+// Joins a sequence that crosses range borders, one CTA per (query head, border):
+// the sequence's first border does the work, four warps taking every fourth
+// partial.  With M = max LSE_s and w_s = exp(LSE_s - M), O = sum w_s O_s / sum w_s and
+// LSE = M + ln sum w_s.  A partial without positions (-inf) has no output; one that is
+// not to be used (+inf) makes the row empty.
 template <int D>
 __global__ void __launch_bounds__(128) decode_fp8_join_kernel(const Decode8Args a) {
   constexpr int kPer = D / 32;
-  const long long rows = static_cast<long long>(a.B) * a.H;
-  const long long row = blockIdx.x;
+  const int h = blockIdx.x, border = blockIdx.y + 1;
   const int warp = warp_id(), lane = lane_id();
   __shared__ float s_max[4], s_w[4];
   __shared__ float s_acc[4][D];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials of the kernel before
+  const int4 at = a.borders[border];  // sequence at the border, tiles before it, its tiles, tiles per range
+  const int b = at.x, begin = at.y, len = at.w;
+  if (b < 0 || begin >= border * len || begin < (border - 1) * len) return;
+  const int parts = (begin + at.z - 1) / len - border + 2;
+  // slot of partial s: the second one of the range in which the sequence begins, then the first ones
+  auto slot = [&](int s) {
+    return (s == 0 ? static_cast<size_t>(border - 1) * 2 + 1 : static_cast<size_t>(border - 1 + s) * 2) * a.H + h;
+  };
   float M = -INFINITY;
-  for (int s = static_cast<int>(threadIdx.x); s < a.splits; s += 128) M = fmaxf(M, a.LSEpart[s * rows + row]);
+  for (int s = static_cast<int>(threadIdx.x); s < parts; s += 128) M = fmaxf(M, a.LSEpart[slot(s)]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   if (lane == 0) s_max[warp] = M;
@@ -563,11 +753,11 @@ __global__ void __launch_bounds__(128) decode_fp8_join_kernel(const Decode8Args 
   for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
   float wsum = 0.f;
 #pragma unroll 4
-  for (int s = warp; s < a.splits; s += 4) {
-    const float ls = a.LSEpart[s * rows + row];
+  for (int s = warp; s < parts; s += 4) {
+    const float ls = a.LSEpart[slot(s)];
     if (ls == -INFINITY || bad) continue;
     const float wgt = expf(ls - base);
-    const float* op = a.Opart + (s * rows + row) * D + lane * kPer;
+    const float* op = a.Opart + slot(s) * D + lane * kPer;
     float v[kPer];
     if constexpr (kPer == 4) {
       const float4 x = *reinterpret_cast<const float4*>(op);
@@ -593,6 +783,7 @@ __global__ void __launch_bounds__(128) decode_fp8_join_kernel(const Decode8Args 
       const int c = lane * kPer + i;
       out[i] = ((s_acc[0][c] + s_acc[1][c]) + (s_acc[2][c] + s_acc[3][c])) * inv;
     }
+    const size_t row = static_cast<size_t>(b) * a.H + h;
     __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.O) + row * D + lane * kPer;
     if constexpr (kPer == 4)
       *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(out[0], out[1]), pack_bf16x2(out[2], out[3]));
@@ -605,15 +796,15 @@ __global__ void __launch_bounds__(128) decode_fp8_join_kernel(const Decode8Args 
 template <int D, int NT>
 cudaError_t launch_nt(const CUtensorMap& tk, const CUtensorMap& tv, const Decode8Args& a, const DevCtl& c,
                       cudaStream_t s) {
-  using C = Cfg8<D>;
+  using C = Cfg8<D, NT>;
   cudaError_t e = cudaFuncSetAttribute(decode_fp8_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  const dim3 grid(a.Hkv * a.hgroups, a.B, a.splits);
+  const dim3 grid(a.Hkv * a.hgroups, a.ranges ? a.ranges : a.B);
   decode_fp8_kernel<D, NT><<<grid, kThreads, C::kSmemBytes, s>>>(tk, tv, a, c);
-  if ((e = cudaGetLastError()) != cudaSuccess || a.splits == 1) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess || a.ranges < 2) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<long long>(a.B) * a.H));
+  cfg.gridDim = dim3(a.H, a.ranges - 1);
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -625,6 +816,8 @@ cudaError_t launch_nt(const CUtensorMap& tk, const CUtensorMap& tv, const Decode
 }
 
 }  // namespace
+
+int decode_fp8_ctas_per_sm(int nt) { return nt == 1 ? Cfg8<128, 1>::kCtas : Cfg8<128, 2>::kCtas; }
 
 cudaError_t launch_decode_fp8(const CUtensorMap& tk, const CUtensorMap& tv, const Decode8Args& a, int d, int nt,
                               const DevCtl& c, cudaStream_t s) {

@@ -138,8 +138,7 @@ struct Decode8Args {
   int B, H, Hkv;
   int page_size, num_pages, max_pages;
   int hgroups;       // CTAs per K/V head: groups of at most 8 * nt query heads
-  int splits;        // chunks of positions per (sequence, head group)
-  int chunk;         // positions per chunk (a multiple of 128)
+  int ranges;        // ranges that the tiles of all sequences are cut into; 0: one sequence per CTA
   int window;        // the query's own position and `window` before it are visible; -1: all
   float scale_log2;  // softmax scale * log2(e)
   const void* Q;
@@ -148,14 +147,18 @@ struct Decode8Args {
   const int* seqlens;
   void* O;           // [B, H, d] bf16
   float* LSE;        // [B, H] natural log
-  float* Opart;      // splits > 1: [splits, B, H, d] fp32, normalised per chunk
-  float* LSEpart;    // splits > 1: [splits, B, H] natural log (-inf: no position; +inf: not to be used)
+  // ranges > 0: partial results of sequences that cross a border, two slots per range
+  float* Opart;      // [ranges, 2, H, d] fp32, normalised
+  float* LSEpart;    // [ranges, 2, H] natural log (-inf: no position; +inf: not to be used)
+  int4* borders;     // [ranges]: sequence at the range's first tile (-1: the range is empty), tiles before
+                     // that sequence, its tiles, tiles per range
 };
 
 // TMA descriptor for an 8-bit paged pool viewed as [num_pages * page_size rows][Hkv * d
 // bytes]: a box of min(page_size, 128) rows x d bytes, swizzled over its d bytes.
 CUresult make_paged_map_u8(CUtensorMap* map, const void* base, int num_pages, int page_size, int Hkv, int d);
 // nt: 8-head column blocks per CTA (1 or 2)
+int decode_fp8_ctas_per_sm(int nt);
 cudaError_t launch_decode_fp8(const CUtensorMap& tk, const CUtensorMap& tv, const Decode8Args& a, int d, int nt,
                               const DevCtl& c, cudaStream_t s);
 

@@ -440,7 +440,8 @@ int fa_cache_read(const void* K_cache, const void* V_cache, const void* kv_scale
  * 0xff, which fa_cache_append writes only in such rows, count as +-480 in a row with
  * another scale byte.  Out-of-range lengths and page indices leave the sequence's rows
  * empty (O = 0, LSE = -inf) and are reported, as in fa_decode_paged.
- *   max_pages * page_size <= 2^30; the other limits as fa_decode_paged.
+ *   max_pages * page_size <= 2^30, B * max_pages * page_size <= 2^37; the other limits as
+ *   fa_decode_paged.
  */
 int fa_decode_paged_fp8(const void* Q, const void* K_cache, const void* V_cache, const void* kv_scale,
                         const int* block_table, const int* seqlens, void* O, float* LSE, int B, int H, int Hkv, int d,

@@ -218,6 +218,7 @@ def test_decode_fp8_validation(L):
     assert call(scale=0.0) == -1 and call(scale=float("nan")) == -1 and call(w=-2) == -1
     assert call(npg=0) == -1 and call(mp=0) == -1 and call(B=-1) == -1
     assert call(npg=1 << 28) == -8 and call(mp=(1 << 26) + 1) == -8 and call(B=65536) == -8
+    assert call(B=256, mp=1 << 26) == -8                          # 2^38 positions in all
     assert call(q=8) == -3 and call(sc=8) == -3
     assert call(ws=8, size=64) == -4
     assert call(B=0, ptr=None) == 0
