@@ -828,11 +828,11 @@ int fa_decode_paged(const void* Q, const void* K_cache, const void* V_cache, con
 // ---------------------------------------------------------------------------
 namespace {
 
-// Warps per launch that keep every SM's warp slots filled about twice over; below
-// that a warp takes fewer row groups of its position.
+// Row groups per warp: as many as the tensor with more heads has, at most 8, but fewer
+// where that leaves less than about two rounds of warps (148 SMs x 64).
 constexpr long long kFullWarps = 148LL * 64;
 constexpr int kRopeBlockWarps = 4;
-constexpr int kRopeBwdBlocks = 148 * 6;
+constexpr int kRopeBwdBlocks = 148 * 3;  // resident together
 
 bool aligned_strides(const long long* s, int dtype) {
   const long long m = dtype == FA_BF16 ? 8 : 4;  // 16 bytes
@@ -851,7 +851,9 @@ int check_rope(const void* Q, const void* K, const void* wq, const void* wk, con
   int rc = check_shape(B, H, N, d, dtype);
   if (rc) return rc;
   if (Hkv < 0 || table_rows < 0) return FA_ERR_INVALID_ARG;
-  if (Hkv > 65535 || static_cast<long long>(B) * N > 0x7fffffffLL) return FA_ERR_TOO_LARGE;
+  if (Hkv > 65535 || static_cast<long long>(B) * N > 0x7fffffffLL ||
+      static_cast<double>(B) * N * Hkv * d >= 1099511627776.0)  // 2^40
+    return FA_ERR_TOO_LARGE;
   if ((interleaved != 0 && interleaved != 1) || (weight_dtype != FA_BF16 && weight_dtype != FA_FP32))
     return FA_ERR_INVALID_ARG;
   if (!std::isfinite(eps) || eps < 0.f) return FA_ERR_INVALID_ARG;
@@ -891,16 +893,17 @@ RopeArgs rope_args(const void* Q, const void* K, const void* wq, const void* wk,
   a.eps = eps;
   a.status = status;
   const int rows = 512 / d;
-  const long long groups = (H + rows - 1) / rows + (Hkv + rows - 1) / rows;
+  const int qg = (H + rows - 1) / rows, kg = (Hkv + rows - 1) / rows;
+  auto warps = [&](int per) { return static_cast<long long>(a.tokens) * ((qg + per - 1) / per + (kg + per - 1) / per); };
   a.per = 8;
-  while (a.per > 1 && a.tokens * ((groups + a.per - 1) / a.per) < kFullWarps) a.per /= 2;
+  while (a.per > 2 && (a.per / 2 >= std::max(qg, kg) || warps(a.per) < kFullWarps)) a.per /= 2;
   a.q_groups = (H + rows * a.per - 1) / (rows * a.per);
   a.k_groups = (Hkv + rows * a.per - 1) / (rows * a.per);
   return a;
 }
 
-// Blocks of the backward: as many as fill the GPU, shared between q and k by their heads.
-void rope_blocks(RopeArgs* a) {
+// Blocks of the backward: as many as fill the GPU, shared between q and k by their work.
+void rope_blocks(RopeArgs* a, int d) {
   const long long qu = static_cast<long long>(a->tokens) * a->q_groups, ku = static_cast<long long>(a->tokens) * a->k_groups;
   const long long qw = (qu + kRopeBlockWarps - 1) / kRopeBlockWarps, kw = (ku + kRopeBlockWarps - 1) / kRopeBlockWarps;
   if (qw + kw <= kRopeBwdBlocks) {
@@ -908,8 +911,11 @@ void rope_blocks(RopeArgs* a) {
     a->blocks = static_cast<int>(qw + kw);
     return;
   }
-  const long long want = static_cast<long long>(kRopeBwdBlocks) * a->H / (a->H + a->Hkv);
-  a->q_blocks = static_cast<int>(std::min(qw, std::max<long long>(a->H ? 1 : 0, std::min<long long>(want, kRopeBwdBlocks - (a->Hkv ? 1 : 0)))));
+  // by their row groups, and one more for each unit's start
+  const int rows = 512 / d;
+  const long long qc = (a->H + rows - 1) / rows + a->q_groups, kc = (a->Hkv + rows - 1) / rows + a->k_groups;
+  const long long want = std::max<long long>(a->H ? 1 : 0, kRopeBwdBlocks * qc / (qc + kc));
+  a->q_blocks = static_cast<int>(std::min(qw, std::min<long long>(want, kRopeBwdBlocks - (a->Hkv ? 1 : 0))));
   a->blocks = a->q_blocks + static_cast<int>(std::min(kw, static_cast<long long>(kRopeBwdBlocks - a->q_blocks)));
 }
 
@@ -969,7 +975,7 @@ int fa_qk_norm_rope_bwd(const void* Q, const void* K, const void* q_weight, cons
   a.k.g = dK_out;
   set_strides(dq_out_strides, N, H, d, &a.q.gb, &a.q.gn, &a.q.gh);
   set_strides(dk_out_strides, N, Hkv, d, &a.k.gb, &a.k.gn, &a.k.gh);
-  if (!empty) rope_blocks(&a);
+  if (!empty) rope_blocks(&a, d);
   a.partial = static_cast<float*>(workspace);
   a.dwq = dq_weight;
   a.dwk = dk_weight;

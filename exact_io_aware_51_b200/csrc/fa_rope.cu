@@ -221,8 +221,7 @@ __device__ __forceinline__ float row_rsqrt(const float2 (&x)[8], float eps) {
 }
 
 // position of a token: -1 for padding; one outside the tables is reported and treated as padding
-__device__ __forceinline__ int token_position(const RopeArgs& a, int token, int n, int lane) {
-  int pos = a.positions ? a.positions[token] : n;
+__device__ __forceinline__ int checked_position(const RopeArgs& a, int pos, int lane) {
   if (pos >= a.table) {
     if (lane == 0) atomicCAS(a.status, 0, kDevBadInput | 0xD3);
     pos = -1;
@@ -234,8 +233,11 @@ __device__ __forceinline__ int token_position(const RopeArgs& a, int token, int 
 // Forward: a warp takes `per` groups of rows (4 heads of d = 128, 8 of d = 64)
 // of one tensor at one position; grid (position blocks, head groups of q then k).
 // ---------------------------------------------------------------------------
-template <typename T, int D, bool kNorm, bool kInter>
-__global__ void __launch_bounds__(kWarps * 32) rope_fwd_kernel(const RopeArgs a) {
+// kAhead rows are loaded before the first is used.  Measured at B1 N16384 H32 + 32 d128
+// bf16 (537 MB): 4 rows at 5 blocks per SM 85 us, 2 rows 95 us; 4 blocks or spilled
+// registers at 6 87..91 us.  A warp with two row groups has no use for four.
+template <typename T, int D, bool kNorm, bool kInter, int kAhead>
+__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 && !kInter ? 5 : 4) rope_fwd_kernel(const RopeArgs a) {
   constexpr int kLanes = D / 16;
   constexpr int kRows = 32 / kLanes;
   const int lane = lane_id();
@@ -250,22 +252,23 @@ __global__ void __launch_bounds__(kWarps * 32) rope_fwd_kernel(const RopeArgs a)
   const RopeTensor& t = is_q ? a.q : a.k;
   const T* x0 = static_cast<const T*>(t.x) + b * t.sb + n * t.sn;
   T* o0 = static_cast<T*>(t.out) + static_cast<size_t>(token) * nh * D;
-  const int pos = token_position(a, token, n, lane);
+  const int pos = checked_position(a, a.positions ? a.positions[token] : n, lane);
   float2 c[4], s[4], w[8];
   if (pos >= 0) load_angles<D, kInter>(a.cos_t, a.sin_t, pos, sub, c, s);
   if (kNorm) load_gain<D>(t.w, a.w_f32, sub, w);
   Coef k;
   if (pos >= 0) make_coef<kInter, kNorm>(c, s, w, k);
-  for (int it = 0; it < a.per; it += 2) {
-    Raw<T> raw[2] = {};
-    const int ha = h0 + it * kRows, hb = ha + kRows;
-    const bool oka = ha < nh, okb = it + 1 < a.per && hb < nh;
-    if (pos >= 0) {
-      if (oka) load_row<D>(raw[0], x0 + ha * t.sh, sub);
-      if (okb) load_row<D>(raw[1], x0 + hb * t.sh, sub);
+  for (int it = 0; it < a.per && (group * a.per + it) * kRows < nh; it += kAhead) {
+    Raw<T> raw[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int h = h0 + (it + u) * kRows;
+      raw[u] = {};
+      if (pos >= 0 && it + u < a.per && h < nh) load_row<D>(raw[u], x0 + h * t.sh, sub);
     }
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < kAhead; ++u) {
+      const int h = h0 + (it + u) * kRows;
       float2 o[8];
       if (pos >= 0) {
         float2 x[8];
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__(kWarps * 32) rope_fwd_kernel(const RopeArgs a)
 #pragma unroll
         for (int j = 0; j < 8; ++j) o[j] = make_float2(0.f, 0.f);
       }
-      if (u == 0 ? oka : okb) store_row<D>(o0 + static_cast<size_t>(u == 0 ? ha : hb) * D, sub, o);
+      if (it + u < a.per && h < nh) store_row<D>(o0 + static_cast<size_t>(h) * D, sub, o);
     }
   }
 }
@@ -291,55 +294,187 @@ __global__ void __launch_bounds__(kWarps * 32) rope_fwd_kernel(const RopeArgs a)
 // others those of k, each warp with its own running sum of the gain's gradient;
 // a block writes the sum of its warps to partial[block][d].
 // ---------------------------------------------------------------------------
+template <typename T, int D, bool kNorm>
+struct BwdRing {
+  // Rows and angles of the next iterations wait in shared memory, written by asynchronous
+  // copies into slots of the lane's own (no barrier): the registers that the
+  // gradient needs leave room for 12 warps on an SM, whose own loads would keep only
+  // 24 KB in flight.
+  static constexpr int kStages = sizeof(T) == 2 ? 4 : 3;
+  static constexpr int kRow = 16 * sizeof(T) / 16;             // 16-byte pieces of a lane's 16 features
+  static constexpr int kPieces = (kNorm ? 2 : 1) * kRow;       // g, then x
+  static constexpr int kBytes = kStages * (kPieces + 4) * kWarps * 32 * 16;
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_l1(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int kPending>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void lds_row(uint32_t addr, Raw<__nv_bfloat16>& r) {
+  const float4 a = lds_f4(addr), b = lds_f4(addr + kWarps * 32 * 16);
+  r.a = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(a.z), __float_as_uint(a.w));
+  r.b = make_uint4(__float_as_uint(b.x), __float_as_uint(b.y), __float_as_uint(b.z), __float_as_uint(b.w));
+}
+__device__ __forceinline__ void lds_row(uint32_t addr, Raw<float>& r) {
+  constexpr int kStep = kWarps * 32 * 16;
+  r.a0 = lds_f4(addr);
+  r.a1 = lds_f4(addr + kStep);
+  r.b0 = lds_f4(addr + 2 * kStep);
+  r.b1 = lds_f4(addr + 3 * kStep);
+}
+// this lane's 16 features of the row at p into its slots from dst on
+template <int D, typename T>
+__device__ __forceinline__ void copy_row(uint32_t dst, const T* p, int sub) {
+  constexpr int kStep = kWarps * 32 * 16;
+  constexpr int kHalf = 8 * sizeof(T) / 16;
+#pragma unroll
+  for (int i = 0; i < kHalf; ++i) {
+    copy16(dst + i * kStep, p + 8 * sub + i * (16 / sizeof(T)));
+    copy16(dst + (kHalf + i) * kStep, p + D / 2 + 8 * sub + i * (16 / sizeof(T)));
+  }
+}
+
+// A warp's walk over its units (a position, a group of rows) and their iterations.
+struct Units {
+  unsigned int u, units, stride;  // unit, their number, step (units + stride < 2^32, host check)
+  int groups, nh, rows;
+  int it, its;        // iteration, iterations of the unit
+  int h0;             // head of this lane's row at iteration 0
+  int token, pos;
+  int coming;         // position of the next unit's token, asked for a unit ahead
+  __device__ __forceinline__ bool more() const { return u < units; }
+  __device__ __forceinline__ int raw_position(const RopeArgs& a, unsigned int unit) const {
+    if (unit >= units) return -1;
+    const int tok = static_cast<int>(unit / static_cast<unsigned int>(groups));
+    return a.positions ? a.positions[tok] : tok % a.N;
+  }
+  __device__ __forceinline__ void open(const RopeArgs& a, int raw, int lane_row, int lane) {  // unit u < units
+    token = static_cast<int>(u / static_cast<unsigned int>(groups));
+    const int first = static_cast<int>(u - static_cast<unsigned int>(token) * groups) * a.per * rows;
+    pos = checked_position(a, raw, lane);
+    coming = raw_position(a, u + stride);
+    its = min(a.per, (nh - first + rows - 1) / rows);
+    h0 = first + lane_row;
+    it = 0;
+  }
+  __device__ __forceinline__ void next(const RopeArgs& a, int lane_row, int lane) {
+    u += stride;
+    if (more()) open(a, coming, lane_row, lane);
+  }
+};
+
 template <typename T, int D, bool kNorm, bool kInter>
-__global__ void __launch_bounds__(kWarps * 32) rope_bwd_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 3) rope_bwd_kernel(const RopeArgs a) {
+  using R = BwdRing<T, D, kNorm>;
+  extern __shared__ __align__(16) uint8_t ring[];
   constexpr int kLanes = D / 16;
   constexpr int kRows = 32 / kLanes;
+  constexpr int kStep = kWarps * 32 * 16;
   const int lane = lane_id(), warp = warp_id();
   const int sub = lane % kLanes;
   const bool is_q = static_cast<int>(blockIdx.x) < a.q_blocks;
   const int first = is_q ? blockIdx.x : blockIdx.x - a.q_blocks;
   const int blocks = is_q ? a.q_blocks : static_cast<int>(gridDim.x) - a.q_blocks;
   const int nh = is_q ? a.H : a.Hkv;
-  const int groups = is_q ? a.q_groups : a.k_groups;
   const RopeTensor& t = is_q ? a.q : a.k;
-  const long long units = static_cast<long long>(a.tokens) * groups;
+  Units at;
+  at.groups = is_q ? a.q_groups : a.k_groups;
+  at.nh = nh;
+  at.rows = kRows;
+  at.units = static_cast<unsigned int>(a.tokens) * static_cast<unsigned int>(at.groups);
+  at.stride = static_cast<unsigned int>(blocks) * kWarps;
+  at.u = static_cast<unsigned int>(first) * kWarps + warp;
+  const uint32_t rows_at = smem_u32(ring) + threadIdx.x * 16;
+  const uint32_t angles_at = rows_at + R::kStages * R::kPieces * kStep;
   float2 w[8], acc[8];
   if (kNorm) load_gain<D>(t.w, a.w_f32, sub, w);
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] = make_float2(0.f, 0.f);
 
-  for (long long u = static_cast<long long>(first) * kWarps + warp; u < units; u += static_cast<long long>(blocks) * kWarps) {
-    const int token = static_cast<int>(u / groups);
-    const int group = static_cast<int>(u - static_cast<long long>(token) * groups);
-    const int b = token / a.N, n = token - b * a.N;
-    const int pos = token_position(a, token, n, lane);
-    const T* x0 = static_cast<const T*>(t.x) + b * t.sb + n * t.sn;
-    const T* g0 = static_cast<const T*>(t.g) + b * t.gb + n * t.gn;
-    T* o0 = static_cast<T*>(t.out) + static_cast<size_t>(token) * nh * D;
+  // the copies of one iteration, as one group (which may be empty)
+  if (at.more()) at.open(a, at.raw_position(a, at.u), lane / kLanes, lane);
+  Units ahead = at;
+  int ahead_row = 0, ahead_unit = 0;  // slots
+  const T* gp = nullptr;
+  const T* xp = nullptr;
+  auto fetch = [&]() {
+    if (ahead.more()) {
+      if (ahead.it == 0) {
+        const int b = ahead.token / a.N, n = ahead.token - b * a.N;
+        gp = static_cast<const T*>(t.g) + b * t.gb + n * t.gn;
+        xp = static_cast<const T*>(t.x) + b * t.sb + n * t.sn;
+        if (ahead.pos >= 0) {
+          const size_t row = static_cast<size_t>(ahead.pos) * (D / 2);
+          const int o0 = kInter ? 4 * sub : 8 * sub, o1 = kInter ? D / 4 + 4 * sub : 8 * sub + 4;
+          const uint32_t dst = angles_at + ahead_unit * 4 * kStep;
+          copy16_l1(dst, a.cos_t + row + o0);
+          copy16_l1(dst + kStep, a.cos_t + row + o1);
+          copy16_l1(dst + 2 * kStep, a.sin_t + row + o0);
+          copy16_l1(dst + 3 * kStep, a.sin_t + row + o1);
+        }
+        ahead_unit = ahead_unit + 1 == R::kStages ? 0 : ahead_unit + 1;
+      }
+      const int h = ahead.h0 + ahead.it * kRows;
+      if (ahead.pos >= 0 && h < nh) {
+        const uint32_t dst = rows_at + ahead_row * R::kPieces * kStep;
+        copy_row<D>(dst, gp + h * t.gh, sub);
+        if (kNorm) copy_row<D>(dst + R::kRow * kStep, xp + h * t.sh, sub);
+      }
+      if (++ahead.it == ahead.its) ahead.next(a, lane / kLanes, lane);
+    }
+    ahead_row = ahead_row + 1 == R::kStages ? 0 : ahead_row + 1;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+#pragma unroll
+  for (int i = 0; i < R::kStages - 1; ++i) fetch();
+  int row_slot = 0, unit_slot = 0;
+  while (at.more()) {
+    T* o0 = static_cast<T*>(t.out) + static_cast<size_t>(at.token) * nh * D;
     float2 c[4], s[4];
-    if (pos >= 0) load_angles<D, kInter>(a.cos_t, a.sin_t, pos, sub, c, s);
-    for (int it = 0; it < a.per; ++it) {
-      const int h = (group * a.per + it) * kRows + lane / kLanes;
+    for (; at.it < at.its; ++at.it) {
+      fetch();
+      copies_wait<R::kStages - 1>();  // the oldest group has arrived
+      if (at.it == 0) {
+        const uint32_t src = angles_at + unit_slot * 4 * kStep;
+        const float4 c0 = lds_f4(src), c1 = lds_f4(src + kStep), s0 = lds_f4(src + 2 * kStep), s1 = lds_f4(src + 3 * kStep);
+        c[0] = make_float2(c0.x, c0.y), c[1] = make_float2(c0.z, c0.w);
+        c[2] = make_float2(c1.x, c1.y), c[3] = make_float2(c1.z, c1.w);
+        s[0] = make_float2(s0.x, s0.y), s[1] = make_float2(s0.z, s0.w);
+        s[2] = make_float2(s1.x, s1.y), s[3] = make_float2(s1.z, s1.w);
+        unit_slot = unit_slot + 1 == R::kStages ? 0 : unit_slot + 1;
+      }
+      const uint32_t src = rows_at + row_slot * R::kPieces * kStep;
+      row_slot = row_slot + 1 == R::kStages ? 0 : row_slot + 1;
+      const int h = at.h0 + at.it * kRows;
       const bool ok = h < nh;
       float2 o[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = make_float2(0.f, 0.f);
-      if (pos >= 0) {
-        Raw<T> rx = {}, rg = {};
-        if (ok) {
-          load_row<D>(rg, g0 + h * t.gh, sub);
-          if (kNorm) load_row<D>(rx, x0 + h * t.sh, sub);
-        }
+      if (at.pos >= 0) {  // what a lane without a row holds stays in its row's lanes
+        Raw<T> raw;
         float2 g[8], gr[8];
-        unpack(rg, g);
+        lds_row(src, raw);
+        unpack(raw, g);
         rotate_back<kInter>(g, c, s, gr);
         if constexpr (!kNorm) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) o[j] = gr[j];
         } else {
           float2 x[8];
-          unpack(rx, x);
+          lds_row(src + R::kRow * kStep, raw);
+          unpack(raw, x);
           const float r = row_rsqrt<D>(x, a.eps);
           float2 dot = make_float2(0.f, 0.f), gx[8];
 #pragma unroll
@@ -358,7 +493,9 @@ __global__ void __launch_bounds__(kWarps * 32) rope_bwd_kernel(const RopeArgs a)
       }
       if (ok) store_row<D>(o0 + static_cast<size_t>(h) * D, sub, o);
     }
+    at.next(a, lane / kLanes, lane);
   }
+  copies_wait<0>();
 
   if constexpr (kNorm) {
     __shared__ float sums[kWarps][D];
@@ -386,52 +523,83 @@ __global__ void __launch_bounds__(kWarps * 32) rope_bwd_kernel(const RopeArgs a)
   }
 }
 
-// dw = sum of the blocks' partial sums, in 64 bits and in a fixed order: block 0 for q, 1 for k
+// dw = sum of the blocks' partial sums, in 64 bits and in a fixed order: grid (q or k,
+// 32 features), 32 x 32 threads of one feature and every 32nd block each
 template <int D>
-__global__ void __launch_bounds__(8 * D) rope_dw_kernel(const float* __restrict__ partial, int q_blocks, int blocks,
-                                                        void* dwq, void* dwk, int w_f32) {
-  __shared__ double sums[8][D];
-  const int f = threadIdx.x % D, part = threadIdx.x / D;
+__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__ partial, int q_blocks, int blocks,
+                                                       void* dwq, void* dwk, int w_f32) {
+  __shared__ double sums[32][33];
+  const int f = lane_id(), part = warp_id();
   const int lo = blockIdx.x ? q_blocks : 0, hi = blockIdx.x ? blocks : q_blocks;
+  const float* p = partial + blockIdx.y * 32 + f;
   double v = 0.0;
-#pragma unroll 4
-  for (int i = lo + part; i < hi; i += 8) v += static_cast<double>(partial[static_cast<size_t>(i) * D + f]);
-  sums[part][f] = v;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums of the kernel before
+#pragma unroll 8
+  for (int i = lo + part; i < hi; i += 32) v += static_cast<double>(__ldcg(p + static_cast<size_t>(i) * D));
+  sums[f][part] = v;
   __syncthreads();
-  if (part == 0) {
+  v = sums[part][f];  // warp `part` now holds feature `part`
 #pragma unroll
-    for (int i = 1; i < 8; ++i) v += sums[i][f];
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (f == 0) {
     void* out = blockIdx.x ? dwk : dwq;
+    const int at = blockIdx.y * 32 + part;
     if (w_f32)
-      static_cast<float*>(out)[f] = static_cast<float>(v);
+      static_cast<float*>(out)[at] = static_cast<float>(v);
     else
-      static_cast<__nv_bfloat16*>(out)[f] = __float2bfloat16_rn(static_cast<float>(v));
+      static_cast<__nv_bfloat16*>(out)[at] = __float2bfloat16_rn(static_cast<float>(v));
   }
+}
+
+template <typename T, int D, bool kNorm, bool kInter>
+void launch_fwd_k(const RopeArgs& a, cudaStream_t s) {
+  const dim3 grid((a.tokens + kWarps - 1) / kWarps, a.q_groups + a.k_groups);
+  constexpr int kMany = sizeof(T) == 2 ? 4 : 2;  // registers
+  if (a.per >= 4) rope_fwd_kernel<T, D, kNorm, kInter, kMany><<<grid, kWarps * 32, 0, s>>>(a);
+  else rope_fwd_kernel<T, D, kNorm, kInter, kMany / 2><<<grid, kWarps * 32, 0, s>>>(a);
 }
 
 template <typename T, int D>
 cudaError_t launch_fwd_d(const RopeArgs& a, cudaStream_t s) {
-  const dim3 grid((a.tokens + kWarps - 1) / kWarps, a.q_groups + a.k_groups);
   const bool norm = a.q.w != nullptr;
-  if (norm && a.interleaved) rope_fwd_kernel<T, D, true, true><<<grid, kWarps * 32, 0, s>>>(a);
-  else if (norm) rope_fwd_kernel<T, D, true, false><<<grid, kWarps * 32, 0, s>>>(a);
-  else if (a.interleaved) rope_fwd_kernel<T, D, false, true><<<grid, kWarps * 32, 0, s>>>(a);
-  else rope_fwd_kernel<T, D, false, false><<<grid, kWarps * 32, 0, s>>>(a);
+  if (norm && a.interleaved) launch_fwd_k<T, D, true, true>(a, s);
+  else if (norm) launch_fwd_k<T, D, true, false>(a, s);
+  else if (a.interleaved) launch_fwd_k<T, D, false, true>(a, s);
+  else launch_fwd_k<T, D, false, false>(a, s);
+  return cudaGetLastError();
+}
+
+template <typename T, int D, bool kNorm, bool kInter>
+cudaError_t launch_bwd_k(const RopeArgs& a, cudaStream_t s) {
+  constexpr int kBytes = BwdRing<T, D, kNorm>::kBytes;
+  const cudaError_t e =
+      cudaFuncSetAttribute(rope_bwd_kernel<T, D, kNorm, kInter>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (e != cudaSuccess) return e;
+  rope_bwd_kernel<T, D, kNorm, kInter><<<a.blocks, kWarps * 32, kBytes, s>>>(a);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
 cudaError_t launch_bwd_d(const RopeArgs& a, cudaStream_t s) {
   const bool norm = a.q.w != nullptr;
+  cudaError_t e = cudaSuccess;
   if (a.blocks == 0) {  // no row: the gains' gradients are still written (zero)
-  } else if (norm && a.interleaved) rope_bwd_kernel<T, D, true, true><<<a.blocks, kWarps * 32, 0, s>>>(a);
-  else if (norm) rope_bwd_kernel<T, D, true, false><<<a.blocks, kWarps * 32, 0, s>>>(a);
-  else if (a.interleaved) rope_bwd_kernel<T, D, false, true><<<a.blocks, kWarps * 32, 0, s>>>(a);
-  else rope_bwd_kernel<T, D, false, false><<<a.blocks, kWarps * 32, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  } else if (norm && a.interleaved) e = launch_bwd_k<T, D, true, true>(a, s);
+  else if (norm) e = launch_bwd_k<T, D, true, false>(a, s);
+  else if (a.interleaved) e = launch_bwd_k<T, D, false, true>(a, s);
+  else e = launch_bwd_k<T, D, false, false>(a, s);
   if (e != cudaSuccess || !norm) return e;
-  rope_dw_kernel<D><<<2, 8 * D, 0, s>>>(a.partial, a.q_blocks, a.blocks, a.dwq, a.dwk, a.w_f32);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2, D / 32);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its start overlaps the end of the kernel before
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, rope_dw_kernel<D>, static_cast<const float*>(a.partial), a.q_blocks, a.blocks, a.dwq,
+                            a.dwk, a.w_f32);
 }
 
 }  // namespace
