@@ -11,10 +11,12 @@
 // (NaN) and NaN codes: the whole row reads back as NaN.  A zero row gets byte 1.
 //
 // Both directions are bound by the bytes they move.  A lane holds 16 features of
-// a row (32 bytes of bf16, 16 of codes), a row takes d / 16 lanes, and a warp
-// takes 4 (d = 128) or 8 (d = 64) consecutive positions of one head, K and V, so
-// the positions' scale bytes, which are neighbours in the pool, are written and
-// read together.
+// a row, 8 from each half, so that neighbouring lanes' 16-byte accesses of bf16 and
+// 8-byte accesses of codes touch whole 32-byte sectors; a row takes d / 16 lanes, and
+// a warp takes 4 (d = 128) or 8 (d = 64) consecutive positions of one head, K and V,
+// so the positions' scale bytes, which are neighbours in the pool, are written and
+// read together.  One group of positions a warp: two or four, loaded ahead, took
+// registers and with them warps away and measured 6 to 20% slower.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -30,16 +32,16 @@ struct Unit {
   int b, n, h;  // sequence, position index of this lane's row, K/V head
 };
 
-// warp -> (sequence, group of positions, head), heads fastest
+// warp -> (sequence, a.per groups of 512 / d positions, head), heads fastest
 template <int D>
 __device__ __forceinline__ bool unit_of(const CacheArgs& a, Unit& u) {
-  constexpr int kRows = 512 / D;
+  const int kRows = 512 / D * a.per;
   const unsigned int w = blockIdx.x * kWarps + warp_id();
   if (w >= a.units) return false;
   const unsigned int t = w / a.Hkv;
   u.h = w - t * a.Hkv;
   u.b = t / a.groups;
-  u.n = (t - u.b * a.groups) * kRows + lane_id() / (D / 16);
+  u.n = static_cast<int>(t - u.b * a.groups) * kRows + lane_id() / (D / 16);
   return true;
 }
 
@@ -92,45 +94,47 @@ __global__ void __launch_bounds__(kWarps * 32) cache_append_kernel(const CacheAr
   const bool fits = start >= 0 && count >= 0 && count <= a.N &&
                     static_cast<long long>(start) + count <= static_cast<long long>(a.max_pages) * a.page_size;
   if (!fits && lane_id() == 0) atomicCAS(a.status, 0, kDevBadInput | 0xD1);
-  const bool ok = fits && u.n < count;
-  uint4 x[2][2];
+  if (!fits) return;
+  constexpr int kRows = 512 / D;
+  const int end = u.n - lane_id() / (D / 16) + a.per * kRows;  // the same for every lane
+  for (int first = end - a.per * kRows; first < min(end, count); first += kRows, u.n += kRows) {
+    const bool ok = u.n < count;
+    uint4 x[2][2];
 #pragma unroll
-  for (int w = 0; w < 2; ++w) x[w][0] = x[w][1] = make_uint4(0u, 0u, 0u, 0u);
-  long long row = -1;
-  int page = 0, slot = 0;
-  if (ok) {
-    const CacheTensor& tk = a.t[0];
-    const CacheTensor& tv = a.t[1];
-    const uint4* pk = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(tk.x) + u.b * tk.sb + u.n * tk.sn +
-                                                     u.h * tk.sh + 16 * sub);
-    const uint4* pv = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(tv.x) + u.b * tv.sb + u.n * tv.sn +
-                                                     u.h * tv.sh + 16 * sub);
-    x[0][0] = pk[0];
-    x[0][1] = pk[1];
-    x[1][0] = pv[0];
-    x[1][1] = pv[1];
-    row = pool_row(a, u.b, start + u.n, &page, &slot);
-  }
+    for (int w = 0; w < 2; ++w) x[w][0] = x[w][1] = make_uint4(0u, 0u, 0u, 0u);
+    long long row = -1;
+    int page = 0, slot = 0;
+    if (ok) {
+      const CacheTensor& tk = a.t[0];
+      const CacheTensor& tv = a.t[1];
+      const uint4* pk = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(tk.x) + u.b * tk.sb +
+                                                       u.n * tk.sn + u.h * tk.sh + 8 * sub);
+      const uint4* pv = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(tv.x) + u.b * tv.sb +
+                                                       u.n * tv.sn + u.h * tv.sh + 8 * sub);
+      x[0][0] = pk[0];
+      x[0][1] = pk[D / 16];
+      x[1][0] = pv[0];
+      x[1][1] = pv[D / 16];
+      row = pool_row(a, u.b, start + u.n, &page, &slot);
+    }
 #pragma unroll
-  for (int w = 0; w < 2; ++w) {
-    const size_t at = (static_cast<size_t>(row) * a.Hkv + u.h) * D + 16 * sub;
-    if constexpr (kFp8) {
-      const uint32_t sb = scale_byte(row_amax_bits<D>(x[w][0], x[w][1]));  // every lane of the warp
-      // 2^-(byte - 127); NaN for byte 255, so that every code is NaN
-      const float inv = sb == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((254u - sb) << 23);
-      if (row >= 0) {
-        uint4 c;
-        c.x = codes4(x[w][0].x, x[w][0].y, inv);
-        c.y = codes4(x[w][0].z, x[w][0].w, inv);
-        c.z = codes4(x[w][1].x, x[w][1].y, inv);
-        c.w = codes4(x[w][1].z, x[w][1].w, inv);
-        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.t[w].pool) + at) = c;
-        if (sub == 0) a.kv_scale[scale_index(a, page, u.h, w, slot)] = static_cast<uint8_t>(sb);
+    for (int w = 0; w < 2; ++w) {
+      const size_t at = (static_cast<size_t>(row) * a.Hkv + u.h) * D + 8 * sub;
+      if constexpr (kFp8) {
+        const uint32_t sb = scale_byte(row_amax_bits<D>(x[w][0], x[w][1]));  // every lane of the warp
+        // 2^-(byte - 127); NaN for byte 255, so that every code is NaN
+        const float inv = sb == 255u ? __uint_as_float(0x7fc00000u) : __uint_as_float((254u - sb) << 23);
+        if (row >= 0) {
+          uint2* p = reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.t[w].pool) + at);
+          p[0] = make_uint2(codes4(x[w][0].x, x[w][0].y, inv), codes4(x[w][0].z, x[w][0].w, inv));
+          p[D / 16] = make_uint2(codes4(x[w][1].x, x[w][1].y, inv), codes4(x[w][1].z, x[w][1].w, inv));
+          if (sub == 0) a.kv_scale[scale_index(a, page, u.h, w, slot)] = static_cast<uint8_t>(sb);
+        }
+      } else if (row >= 0) {
+        uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.t[w].pool) + at);
+        p[0] = x[w][0];
+        p[D / 16] = x[w][1];
       }
-    } else if (row >= 0) {
-      uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.t[w].pool) + at);
-      p[0] = x[w][0];
-      p[1] = x[w][1];
     }
   }
 }
@@ -171,38 +175,41 @@ __global__ void __launch_bounds__(kWarps * 32) cache_read_kernel(const CacheArgs
 #pragma unroll
   for (int w = 0; w < 2; ++w) y[w][0] = y[w][1] = make_uint4(0u, 0u, 0u, 0u);
   if (row >= 0) {
-    const size_t at = (static_cast<size_t>(row) * a.Hkv + u.h) * D + 16 * sub;
+    const size_t at = (static_cast<size_t>(row) * a.Hkv + u.h) * D + 8 * sub;
     if constexpr (kFp8) {
-      uint4 c[2];
+      uint2 c[2][2];
       uint32_t sb[2];
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        c[w] = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.t[w].pool) + at);
+        const uint2* p = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.t[w].pool) + at);
+        c[w][0] = p[0];
+        c[w][1] = p[D / 16];
         sb[w] = a.kv_scale[scale_index(a, page, u.h, w, slot)];
       }
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         const float sc = scale_value(sb[w]);
-        const uint2 p0 = values4(c[w].x, sc), p1 = values4(c[w].y, sc), p2 = values4(c[w].z, sc),
-                    p3 = values4(c[w].w, sc);
-        y[w][0] = make_uint4(p0.x, p0.y, p1.x, p1.y);
-        y[w][1] = make_uint4(p2.x, p2.y, p3.x, p3.y);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint2 p0 = values4(c[w][i].x, sc), p1 = values4(c[w][i].y, sc);
+          y[w][i] = make_uint4(p0.x, p0.y, p1.x, p1.y);
+        }
       }
     } else {
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
         const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.t[w].pool) + at);
         y[w][0] = p[0];
-        y[w][1] = p[1];
+        y[w][1] = p[D / 16];
       }
     }
   }
-  const size_t to = ((static_cast<size_t>(u.b) * a.N + u.n) * a.Hkv + u.h) * D + 16 * sub;
+  const size_t to = ((static_cast<size_t>(u.b) * a.N + u.n) * a.Hkv + u.h) * D + 8 * sub;
 #pragma unroll
   for (int w = 0; w < 2; ++w) {
     uint4* p = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.t[w].out) + to);
     p[0] = y[w][0];
-    p[1] = y[w][1];
+    p[D / 16] = y[w][1];
   }
 }
 

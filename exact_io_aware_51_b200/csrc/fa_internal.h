@@ -206,7 +206,8 @@ struct CacheArgs {
   const int* start;      // [B] append: the position of the first new row; read: seqlens
   const int* count;      // [B] append: new rows of each sequence, nullptr: N
   int N, Hkv, page_size, page_shift, num_pages, max_pages;
-  unsigned int units, groups;  // warps; groups of 512 / d positions per sequence
+  int per;                     // groups of 512 / d positions that a warp takes one after the other
+  unsigned int units, groups;  // warps; warps per sequence and head
   int* status;
 };
 cudaError_t launch_cache(const CacheArgs& a, int d, bool fp8, bool append, cudaStream_t s);

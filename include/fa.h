@@ -409,7 +409,7 @@ size_t fa_qk_norm_rope_workspace_size(int d);
  * rows of a call must not share a slot (two sequences with a page in common): which
  * one is kept, and whether whole, is not specified.
  *   page_size a power of two from 8 to 4096, d 64 or 128 (FA_ERR_UNSUPPORTED otherwise);
- *   num_pages * page_size < 2^31, max_pages * page_size <= 2^30, B, Hkv <= 65535.
+ *   num_pages * page_size < 2^31, max_pages * page_size <= 2^30, N <= 2^30, B, Hkv <= 65535.
  */
 int fa_cache_append(const void* K, const void* V, void* K_cache, void* V_cache, void* kv_scale, const int* block_table,
                     const int* start, const int* count, int B, int N, int Hkv, int d, const long long* k_strides,

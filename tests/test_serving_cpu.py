@@ -195,7 +195,7 @@ def test_cache_validation(L):
             assert f(P=P) == -2, P
         assert f(B=-1) == -1 and f(N=-1) == -1 and f(Hkv=0) == -1 and f(npg=0) == -1 and f(mp=0) == -1 and f(fp8=2) == -1
         assert f(npg=1 << 27) == -8 and f(mp=(1 << 26) + 1) == -8 and f(B=65536) == -8 and f(Hkv=65536) == -8
-        assert f(B=65535, N=1 << 24, Hkv=64) == -8
+        assert f(B=65535, N=1 << 24, Hkv=64) == -8 and f(N=(1 << 30) + 1) == -8
         for name in ("K", "V", "kc", "vc", "sc", "bt"):
             assert f(**{name: None}) == -1, name
         for name in ("K", "V", "kc", "vc", "sc"):
