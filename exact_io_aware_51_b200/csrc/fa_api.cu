@@ -1128,7 +1128,7 @@ Decode8Plan decode8_plan(int B, int H, int Hkv, int d, int page_size, int max_pa
   // a window's first position lies anywhere in its first tile
   if (window >= 0) span = std::min(span, static_cast<long long>(window) + 1 + 127);
   const long long tiles = (span + 127) / 128;
-  const long long slots = 148LL * fa::decode_fp8_ctas_per_sm(p.nt);
+  const long long slots = 148LL * fa::decode_fp8_ctas_per_sm(d, p.nt);
   const long long per_range = static_cast<long long>(Hkv) * p.hgroups;
   if (tiles <= kDecode8WholeTiles || B == 0) return p;
   long long want = std::max(1LL, slots / per_range);

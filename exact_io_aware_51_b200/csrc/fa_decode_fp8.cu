@@ -61,10 +61,10 @@ template <int D, int NT>
 struct Cfg8 {
   static constexpr int kTileBytes = kTileKeys * D;
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kStages = (D == 128 ? 2 : 4) + (NT == 2 && D == 128 ? 1 : 0);
-  static constexpr int kCtas = NT == 1 ? 3 : 2;                  // per SM
+  static constexpr int kCtas = NT == 2 ? 2 : D == 128 ? 3 : 4;   // per SM
+  static constexpr int kStages = NT == 2 ? (D == 128 ? 3 : 4) : (D == 128 ? 2 : 3);
   static constexpr int kBlocks = NT == 1 ? 2 : 1;                // blocks of 16 positions that a warp takes at a time (registers)
-  static constexpr int kRounds = NT * (D / 64);                  // the merge goes through in slices of the features
+  static constexpr int kRounds = NT == 1 ? 2 : D / 32;                  // the merge goes through in slices of the features
   static constexpr int kSlice = D / kRounds;
   static constexpr int kORow = kSlice + 4;
   static constexpr int kOffScale = kStages * kStageBytes;        // [stage][256] scale bytes
@@ -647,8 +647,10 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
         const float f = scalbnf(ex2(mq[nt][i] - head_max(nt * 8 + 2 * t4 + i)), eref - 127 - kPShift);
         of[nt][i] = eref == 255 ? __uint_as_float(0x7fc00000u) : mt[nt][i] == -INFINITY ? 1.f : f;
       }
-    // head and features of this thread in every slice
-    constexpr int kPer = C::kSlice * 8 * NT / (kConsumers * 32);
+    // head and features of this thread in every slice (threads past the last head have none)
+    constexpr int kPer = 4;
+    static_assert(C::kSlice * 8 * NT / kPer <= kConsumers * 32, "a thread takes four features of one head");
+    static_assert(kConsumers * 32 / (C::kSlice / kPer) <= 16, "heads of the statistics block");
     const int h = threadIdx.x / (C::kSlice / kPer);
     const int c0 = threadIdx.x % (C::kSlice / kPer) * kPer;
     const float M = head_max(h);
@@ -685,30 +687,27 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
           }
       sync_consumers();
       if (h < gv) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (!none) {
 #pragma unroll
-        for (int c = 0; c < kPer; c += 4) {
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (!none) {
-#pragma unroll
-            for (int i = 0; i < kConsumers; ++i) {
-              const float4 x = *reinterpret_cast<const float4*>(ob + (i * 8 * NT + h) * C::kORow + c0 + c);
-              v.x += x.x;
-              v.y += x.y;
-              v.z += x.z;
-              v.w += x.w;
-            }
-            v.x *= inv;
-            v.y *= inv;
-            v.z *= inv;
-            v.w *= inv;
+          for (int i = 0; i < kConsumers; ++i) {
+            const float4 x = *reinterpret_cast<const float4*>(ob + (i * 8 * NT + h) * C::kORow + c0);
+            v.x += x.x;
+            v.y += x.y;
+            v.z += x.z;
+            v.w += x.w;
           }
-          const int f = rd * C::kSlice + c0 + c;
-          if (whole) {
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + row * D + f) =
-                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-          } else if (!none) {
-            *reinterpret_cast<float4*>(a.Opart + part * D + f) = v;
-          }
+          v.x *= inv;
+          v.y *= inv;
+          v.z *= inv;
+          v.w *= inv;
+        }
+        const int f = rd * C::kSlice + c0;
+        if (whole) {
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.O) + row * D + f) =
+              make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        } else if (!none) {
+          *reinterpret_cast<float4*>(a.Opart + part * D + f) = v;
         }
       }
     }
@@ -817,7 +816,10 @@ cudaError_t launch_nt(const CUtensorMap& tk, const CUtensorMap& tv, const Decode
 
 }  // namespace
 
-int decode_fp8_ctas_per_sm(int nt) { return nt == 1 ? Cfg8<128, 1>::kCtas : Cfg8<128, 2>::kCtas; }
+int decode_fp8_ctas_per_sm(int d, int nt) {
+  if (d == 128) return nt == 1 ? Cfg8<128, 1>::kCtas : Cfg8<128, 2>::kCtas;
+  return nt == 1 ? Cfg8<64, 1>::kCtas : Cfg8<64, 2>::kCtas;
+}
 
 cudaError_t launch_decode_fp8(const CUtensorMap& tk, const CUtensorMap& tv, const Decode8Args& a, int d, int nt,
                               const DevCtl& c, cudaStream_t s) {

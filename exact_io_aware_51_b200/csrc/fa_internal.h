@@ -158,7 +158,7 @@ struct Decode8Args {
 // bytes]: a box of min(page_size, 128) rows x d bytes, swizzled over its d bytes.
 CUresult make_paged_map_u8(CUtensorMap* map, const void* base, int num_pages, int page_size, int Hkv, int d);
 // nt: 8-head column blocks per CTA (1 or 2)
-int decode_fp8_ctas_per_sm(int nt);
+int decode_fp8_ctas_per_sm(int d, int nt);
 cudaError_t launch_decode_fp8(const CUtensorMap& tk, const CUtensorMap& tv, const Decode8Args& a, int d, int nt,
                               const DevCtl& c, cudaStream_t s);
 
