@@ -616,6 +616,8 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
       if (lane == 0) mbar_arrive(&bars->empty[st]);
     }
 
+    // the last tile has been multiplied: the join may be brought up (it waits for this grid's end)
+    if (walk.left == walk.n) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // ---- merge the four warps ----
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -719,12 +721,14 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
 
 // Joins a sequence that crosses range borders, one CTA per (query head, border):
 // the sequence's first border does the work, four warps taking every fourth
-// partial.  With M = max LSE_s and w_s = exp(LSE_s - M), O = sum w_s O_s / sum w_s and
-// LSE = M + ln sum w_s.  A partial without positions (-inf) has no output; one that is
-// not to be used (+inf) makes the row empty.
+// partial, each with a running maximum of its own so that statistics and outputs are
+// asked for together.  With M = max LSE_s and w_s = exp(LSE_s - M), O = sum w_s O_s / sum
+// w_s and LSE = M + ln sum w_s.  A partial without positions (-inf) has no output; one
+// that is not to be used (+inf) makes the row empty.
 template <int D>
 __global__ void __launch_bounds__(128) decode_fp8_join_kernel(const Decode8Args a) {
   constexpr int kPer = D / 32;
+  constexpr int kAhead = 4;
   const int h = blockIdx.x, border = blockIdx.y + 1;
   const int warp = warp_id(), lane = lane_id();
   __shared__ float s_max[4], s_w[4];
@@ -738,57 +742,82 @@ __global__ void __launch_bounds__(128) decode_fp8_join_kernel(const Decode8Args 
   auto slot = [&](int s) {
     return (s == 0 ? static_cast<size_t>(border - 1) * 2 + 1 : static_cast<size_t>(border - 1 + s) * 2) * a.H + h;
   };
-  float M = -INFINITY;
-  for (int s = static_cast<int>(threadIdx.x); s < parts; s += 128) M = fmaxf(M, a.LSEpart[slot(s)]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) s_max[warp] = M;
-  __syncthreads();
-  M = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
-  const bool bad = M == INFINITY;
-  const float base = M == -INFINITY ? 0.f : M;
+  float M = -INFINITY, wsum = 0.f;
   float acc[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-  float wsum = 0.f;
-#pragma unroll 4
-  for (int s = warp; s < parts; s += 4) {
-    const float ls = a.LSEpart[slot(s)];
-    if (ls == -INFINITY || bad) continue;
-    const float wgt = expf(ls - base);
-    const float* op = a.Opart + slot(s) * D + lane * kPer;
-    float v[kPer];
-    if constexpr (kPer == 4) {
-      const float4 x = *reinterpret_cast<const float4*>(op);
-      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-    } else {
-      const float2 x = *reinterpret_cast<const float2*>(op);
-      v[0] = x.x, v[1] = x.y;
-    }
-    wsum += wgt;
+  for (int s0 = warp; s0 < parts; s0 += 4 * kAhead) {
+    float ls[kAhead], v[kAhead][kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) acc[i] += wgt * v[i];
+    for (int k = 0; k < kAhead; ++k) {
+      const int s = s0 + 4 * k;
+      ls[k] = -INFINITY;
+      if (s < parts) {
+        ls[k] = __ldcg(a.LSEpart + slot(s));
+        const float* op = a.Opart + slot(s) * D + lane * kPer;  // not written where the statistic is infinite: not used then
+        if constexpr (kPer == 4) {
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(op));
+          v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
+        } else {
+          const float2 x = __ldcg(reinterpret_cast<const float2*>(op));
+          v[k][0] = x.x, v[k][1] = x.y;
+        }
+      }
+    }
+    float m = M;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) m = fmaxf(m, ls[k]);
+    if (m == INFINITY) {  // not to be used; nothing that follows changes it
+      M = m;
+      break;
+    }
+    const float base = m == -INFINITY ? 0.f : m;
+    const float al = M == -INFINITY ? 1.f : expf(M - base);  // with M = -inf there is nothing, or NaN
+    M = m;
+    wsum *= al;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) acc[i] *= al;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (ls[k] == -INFINITY) continue;
+      const float wgt = expf(ls[k] - base);
+      wsum += wgt;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) acc[i] += wgt * v[k][i];
+    }
   }
 #pragma unroll
   for (int i = 0; i < kPer; ++i) s_acc[warp][lane * kPer + i] = acc[i];
-  if (lane == 0) s_w[warp] = wsum;
+  if (lane == 0) {
+    s_max[warp] = M;
+    s_w[warp] = wsum;
+  }
   __syncthreads();
   if (warp == 0) {
-    const float W = (s_w[0] + s_w[1]) + (s_w[2] + s_w[3]);
-    const float inv = W == 0.f ? 0.f : 1.f / W;
-    float out[kPer];
+    M = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+    const bool bad = M == INFINITY;
+    const float base = M == -INFINITY ? 0.f : M;
+    float W = 0.f, out[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int c = lane * kPer + i;
-      out[i] = ((s_acc[0][c] + s_acc[1][c]) + (s_acc[2][c] + s_acc[3][c])) * inv;
+    for (int i = 0; i < kPer; ++i) out[i] = 0.f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float f = s_max[u] == -INFINITY ? 1.f : expf(s_max[u] - base);
+      W += s_w[u] * f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) out[i] += s_acc[u][lane * kPer + i] * f;
     }
+    const bool none = bad || W == 0.f;
+    const float inv = none ? 0.f : 1.f / W;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) out[i] = none ? 0.f : out[i] * inv;
     const size_t row = static_cast<size_t>(b) * a.H + h;
     __nv_bfloat16* p = static_cast<__nv_bfloat16*>(a.O) + row * D + lane * kPer;
     if constexpr (kPer == 4)
       *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(out[0], out[1]), pack_bf16x2(out[2], out[3]));
     else
       *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(out[0], out[1]);
-    if (lane == 0) a.LSE[row] = W == 0.f ? -INFINITY : base + logf(W);
+    if (lane == 0) a.LSE[row] = none ? -INFINITY : base + logf(W);
   }
 }
 
