@@ -750,7 +750,7 @@ def _readable(g):
     sb, sn, sh, sd = g.stride()
     if sd == 1 and sb % unit == 0 and sn % unit == 0 and sh % unit == 0 and g.data_ptr() % 16 == 0:
         return g
-    return g.contiguous()
+    return g.clone(memory_format=torch.contiguous_format)
 
 
 class _QKNormRope(torch.autograd.Function):
@@ -776,7 +776,8 @@ class _QKNormRope(torch.autograd.Function):
 def qk_norm_rope(q, k, cos, sin, q_weight=None, k_weight=None, positions=None, eps: float = 1e-6,
                  interleaved: bool = False):
     """Differentiable ``qk_norm_rope_fwd`` (gradients of q, k and the gains; the tables get none): the step before
-    ``attention``."""
+    ``attention``.  As with any autograd function, capture its backward into a CUDA graph only while no eager graph of
+    the same leaves is alive (PyTorch accumulates into a leaf on the stream of the graph that saw it first)."""
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k, q_weight, k_weight)):
         return _QKNormRope.apply(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
     return qk_norm_rope_fwd(q, k, cos, sin, q_weight, k_weight, positions, eps, interleaved)

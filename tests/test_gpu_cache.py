@@ -246,6 +246,33 @@ def test_table_entries_past_the_end_are_not_read():
 
 
 @pytest.mark.gpu
+def test_pools_beyond_32_bit_offsets():
+    """Pools of 5 GB each (K, V), the sequences' pages at their far end: append, read and decode."""
+    need_gpu()
+    P, Hkv, d = 16, 8, 128
+    pages = 5 * 2 ** 30 // (P * Hkv * d)
+    kc, vc = (torch.empty((pages, P, Hkv, d), dtype=torch.uint8, device="cuda") for _ in range(2))
+    sc = torch.empty((pages, Hkv, 2, P), dtype=torch.uint8, device="cuda")
+    assert kc.numel() > 2 ** 32 and sc.numel() > 2 ** 25
+    g = torch.Generator().manual_seed(35)
+    table = (pages - 1 - torch.arange(6, dtype=torch.int32)).view(2, 3).cuda()
+    k, v = _rows((2, 40, Hkv, d), g).cuda(), _rows((2, 40, Hkv, d), g).cuda()
+    start = torch.zeros(2, dtype=torch.int32, device="cuda")
+    fa.cache_append(k, v, kc, vc, table, start, kv_scale=sc)
+    lens = torch.tensor([40, 33], dtype=torch.int32, device="cuda")
+    near = torch.arange(6, dtype=torch.int32, device="cuda").view(2, 3)  # the same rows in small pools
+    small = [torch.zeros((6, P, Hkv, d), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    ssc = torch.zeros((6, Hkv, 2, P), dtype=torch.uint8, device="cuda")
+    fa.cache_append(k, v, *small, near, start, kv_scale=ssc)
+    for a, b in zip(fa.cache_read(kc, vc, table, lens, 40, kv_scale=sc), fa.cache_read(*small, near, lens, 40, kv_scale=ssc)):
+        assert torch.equal(a, b) and torch.count_nonzero(a[0, 39]) > 0
+    q = torch.randn((2, 16, d), generator=g).to(torch.bfloat16).cuda()
+    for a, b in zip(fa.decode_paged_fp8(q, kc, vc, sc, table, lens), fa.decode_paged_fp8(q, *small, ssc, near, lens)):
+        assert torch.equal(a, b)
+    assert fa.last_device_status()[0] == 0
+
+
+@pytest.mark.gpu
 def test_empty_calls():
     need_gpu()
     kc = torch.zeros((2, 8, 2, 64), dtype=torch.uint8, device="cuda")

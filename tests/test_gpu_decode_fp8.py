@@ -215,6 +215,10 @@ def test_pages_before_the_window_are_not_looked_up():
     need_gpu()
     args = _make(2, 8, 2, 128, 16, [700, 300], seed=13)
     q, kc, vc, sc, table, sl = args
+    whole = _run(args)
+    for w in (699, 2 ** 20, 2 ** 40):                 # windows longer than every sequence
+        got = _run(args, window_left=w)
+        assert torch.equal(got[0], whole[0]) and torch.equal(got[1], whole[1])
     want = _run(args, window_left=100)
     t = table.clone()
     for b, n in enumerate((700, 300)):
@@ -244,6 +248,24 @@ def test_full_size_sampled_sequences():
         local = torch.arange(n, dtype=torch.int32).view(1, n)
         args = (q[b:b + 1].cpu(), kc[pg].cpu(), vc[pg].cpu(), sc[pg].cpu(), local, sl[b:b + 1].cpu())
         _check(args, o[b:b + 1], lse[b:b + 1], 1 / math.sqrt(128))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_sequences_share_the_ranges(d):
+    """More sequences than threads look them up, most of them short or empty, a few long: every way for a
+    sequence to lie in the ranges (several in one, one in several, ending on a border)."""
+    need_gpu()
+    g = torch.Generator().manual_seed(15)
+    lens = torch.randint(0, 40, (400,), generator=g).tolist()
+    for b, n in ((0, 0), (7, 1500), (8, 128), (9, 640), (200, 2900), (399, 900)):
+        lens[b] = n
+    args = _make(400, 2, 1, d, 16, lens, seed=15)
+    assert fa.decode_fp8_workspace_size(400, 2, 1, d, 16, args[4].shape[1]) > 0
+    o, lse = _run(args, scale=0.1)
+    _check(args, o, lse, 0.1)
+    o, lse = _run(args, scale=0.1, window_left=300)
+    _check(args, o, lse, 0.1, 300)
 
 
 @pytest.mark.gpu

@@ -210,6 +210,12 @@ def test_autograd_of_broadcast_and_missing_gradients():
     one = torch.ones_like(q)
     _check_bwd(q, w[0], cos, sin, pos, False, one, q.grad, w[0].grad)
     assert torch.count_nonzero(k.grad) == 0 and torch.count_nonzero(w[1].grad) == 0
+    # a gradient that the kernels cannot read in place: an odd offset, then transposed features
+    for g in (torch.randn(q.numel() + 1, device="cuda").to(BF)[1:].view(q.shape),
+              torch.randn((*q.shape[:2], q.shape[3], q.shape[2]), device="cuda").to(BF).transpose(2, 3)):
+        qo, _ = fa.qk_norm_rope(q, k, cos, sin, w[0], w[1], pos)
+        dq, dw = torch.autograd.grad(qo, (q, w[0]), g)
+        _check_bwd(q, w[0], cos, sin, pos, False, g, dq, dw)
     # one leaf alone
     k2 = k.detach().requires_grad_(True)
     _, ko = fa.qk_norm_rope(q.detach(), k2, cos, sin, w[0].detach(), w[1].detach(), pos)
