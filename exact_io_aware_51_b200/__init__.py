@@ -552,106 +552,32 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None, window=
 # --------------------------------------------------------------------------
 # Around the attention: norm and rotation of query and key heads, the paged cache
 # --------------------------------------------------------------------------
-_StrideArray = ctypes.c_longlong * 3
+_BINDING = None
 
 
-# Plain lookups: torch.cuda.current_stream builds a Stream object, 2 us a call
-_current_handle = torch._C._cuda_getCurrentRawStream
-_NO_CUDA = "tensors must live on a CUDA device (there is no CPU path)"
+def _native():
+    """The C++ side of these calls (``_binding.so``, csrc/binding.cpp): argument checks, outputs, the C call."""
+    global _BINDING
+    if _BINDING is None:
+        L = lib()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise FAError(-6, f"{_PKG / '_binding.so'} cannot be loaded ({e}); build it with "
+                              "`python -m exact_io_aware_51_b200.build`") from e
+        _binding.init(FAError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            L.fa_qk_norm_rope, L.fa_qk_norm_rope_bwd, L.fa_qk_norm_rope_workspace_size, L.fa_cache_append,
+            L.fa_cache_read, L.fa_decode_paged_fp8, L.fa_decode_fp8_workspace_size)))
+        _BINDING = _binding
+    return _BINDING
 
 
-def _elsewhere(index, stream):
-    return stream is not None or torch._C._cuda_getDevice() != index
-
-
-def _empty(shape, strides, dtype, device):
-    """torch.empty by way of empty_strided, which takes 1 us less."""
-    return torch.empty_strided(shape, strides, dtype=dtype, device=device)
-
-
-def _reenter(device, stream, call):
-    """``call()`` with ``device`` current and, if given, ``stream``: what it allocates comes from the stream that the
-    kernels run on, so the memory of a temporary is only handed out again behind them."""
-    if stream is not None and stream.device != device:
+def _on_stream(tensor, stream, call, *args):
+    """``call(*args)`` with ``stream`` current: outputs and scratch come from it, too."""
+    if stream.device != tensor.device:
         raise ValueError("stream belongs to another device than the tensors")
-    with torch.cuda.device(device):
-        if stream is None:
-            return call()
-        with torch.cuda.stream(stream):
-            return call()
-
-
-def _strides(t, name):
-    """None for a dense [B, N, heads, d] tensor, else its (batch, position, head) strides for the C call."""
-    if t.is_contiguous() or t.numel() == 0:
-        return None
-    B, N, h, _ = t.shape
-    sb, sn, sh, sd = t.stride()
-    if sd != 1:
-        raise ValueError(f"{name}: the features of a head must be contiguous")
-    if B == 1:
-        sb = 0
-    if N == 1:
-        sn = 0
-    if h == 1:
-        sh = 0
-    if (sb | sn | sh) & (16 // t.element_size() - 1):
-        raise ValueError(f"{name}: strides must be multiples of 16 bytes")
-    return _StrideArray(sb, sn, sh)
-
-
-def _check_out(out, shape, dtype, device, name):
-    if out.shape != torch.Size(shape) or out.dtype != dtype or out.device != device or not out.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
-
-
-def _rope_check(q, k, cos, sin, q_weight, k_weight, positions):
-    q_shape, k_shape, cos_shape, index, dt = q.shape, k.shape, cos.shape, q.get_device(), q.dtype
-    if len(q_shape) != 4 or len(k_shape) != 4:
-        raise ValueError("expected q [B, N, H, d] and k [B, N, Hkv, d]")
-    B, N, H, d = q_shape
-    kB, kN, Hkv, kd = k_shape
-    if kB != B or kN != N or kd != d:
-        raise ValueError("q and k must agree in batch, positions and head dim")
-    dtype = wdtype = _dtype_code(q)
-    if k.dtype != dt:
-        raise TypeError("q and k must have one dtype")
-    if cos.dtype != torch.float32 or sin.dtype != torch.float32:
-        raise TypeError("cos and sin must be float32")
-    if len(cos_shape) != 2 or cos_shape[1] * 2 != d or sin.shape != cos_shape:
-        raise ValueError("cos and sin must be [positions, d / 2] tables")
-    if not (cos.is_contiguous() and sin.is_contiguous()):
-        raise ValueError("cos and sin must be contiguous")
-    same = k.get_device() == index and cos.get_device() == index and sin.get_device() == index
-    if q_weight is not None and k_weight is not None:
-        wdtype = _dtype_code(q_weight)
-        if k_weight.dtype != q_weight.dtype:
-            raise TypeError("q_weight and k_weight must have one dtype")
-        if q_weight.shape != (d,) or k_weight.shape != (d,):
-            raise ValueError("q_weight and k_weight must be [d]")
-        if not (q_weight.is_contiguous() and k_weight.is_contiguous()):
-            raise ValueError("q_weight and k_weight must be contiguous")
-        same = same and q_weight.get_device() == index and k_weight.get_device() == index
-    elif q_weight is not None or k_weight is not None:
-        raise ValueError("give both gains or none")
-    if positions is None:
-        if N > cos_shape[0] and B > 0:
-            raise ValueError("the tables have fewer rows than there are positions")
-    else:
-        if positions.dtype != torch.int32:
-            raise TypeError("positions must be int32")
-        if positions.shape != (B, N) or not positions.is_contiguous():
-            raise ValueError("positions must be a contiguous [B, N] tensor")
-        same = same and positions.get_device() == index
-    if not same:
-        raise ValueError("all tensors must share one device")
-    if index < 0:
-        raise ValueError(_NO_CUDA)
-    return index, B, N, H, Hkv, d, cos_shape[0], dtype, wdtype
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+    with torch.cuda.stream(stream):
+        return call(*args)
 
 
 def rope_tables(positions: int, d: int, base: float = 10000.0, device="cuda"):
@@ -660,6 +586,14 @@ def rope_tables(positions: int, d: int, base: float = 10000.0, device="cuda"):
     freq = float(base) ** (-torch.arange(0, d, 2, dtype=torch.float64, device=device) / d)
     angle = torch.arange(positions, dtype=torch.float64, device=device)[:, None] * freq
     return angle.cos().float(), angle.sin().float()
+
+
+def qk_norm_rope(q, k, cos, sin, q_weight=None, k_weight=None, positions=None, eps: float = 1e-6,
+                 interleaved: bool = False):
+    """Differentiable ``qk_norm_rope_fwd`` (gradients of q, k and the gains; the tables get none): the step before
+    ``attention``.  As with any autograd function, capture its backward into a CUDA graph only while no eager graph of
+    the same leaves is alive (PyTorch accumulates into a leaf on the stream of the graph that saw it first)."""
+    return _native().norm_rope(q, k, cos, sin, q_weight, k_weight, positions, eps, interleaved)
 
 
 def qk_norm_rope_fwd(q, k, cos, sin, q_weight=None, k_weight=None, positions=None, eps: float = 1e-6,
@@ -673,30 +607,9 @@ def qk_norm_rope_fwd(q, k, cos, sin, q_weight=None, k_weight=None, positions=Non
     ``positions``: [B, N] int32 (negative: padding, a zero row), None: 0 .. N - 1.
     ``interleaved``: pairs (2i, 2i + 1) instead of (i, i + d / 2).
     """
-    index, B, N, H, Hkv, d, rows, dt, wdt = _rope_check(q, k, cos, sin, q_weight, k_weight, positions)
-    if q_out is not None:
-        _check_out(q_out, (B, N, H, d), q.dtype, q.device, "q_out")
-    if k_out is not None:
-        _check_out(k_out, (B, N, Hkv, d), q.dtype, q.device, "k_out")
-    if _elsewhere(index, stream):
-        return _reenter(q.device, stream, lambda: qk_norm_rope_fwd(q, k, cos, sin, q_weight, k_weight, positions, eps,
-                                                                 interleaved, q_out, k_out))
-    return _rope_fwd((index, B, N, H, Hkv, d, rows, dt, wdt), q, k, cos, sin, q_weight, k_weight, positions, eps,
-                     interleaved, q_out, k_out)
-
-
-def _rope_fwd(checked, q, k, cos, sin, q_weight, k_weight, positions, eps, interleaved, q_out=None, k_out=None):
-    """qk_norm_rope_fwd on tensors that _rope_check has seen, on the current device and stream."""
-    index, B, N, H, Hkv, d, rows, dt, wdt = checked
-    qo = torch.empty_like(q, memory_format=torch.contiguous_format) if q_out is None else q_out
-    ko = torch.empty_like(k, memory_format=torch.contiguous_format) if k_out is None else k_out
-    rc = lib().fa_qk_norm_rope(q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), cos.data_ptr(),
-                               sin.data_ptr(), _ptr(positions), qo.data_ptr(), ko.data_ptr(), B, N, H, Hkv, d,
-                               _strides(q, "q"), _strides(k, "k"), rows, eps, 1 if interleaved else 0, dt, wdt,
-                               _current_handle(index))
-    if rc != 0:
-        raise FAError(rc, "fa_qk_norm_rope")
-    return qo, ko
+    args = (q, k, cos, sin, q_weight, k_weight, positions, eps, interleaved, q_out, k_out)
+    call = _native().norm_rope_fwd
+    return call(*args) if stream is None else _on_stream(q, stream, call, *args)
 
 
 def qk_norm_rope_bwd(q, k, cos, sin, dq_out, dk_out, q_weight=None, k_weight=None, positions=None, eps: float = 1e-6,
@@ -704,122 +617,9 @@ def qk_norm_rope_bwd(q, k, cos, sin, dq_out, dk_out, q_weight=None, k_weight=Non
     """Backward of ``qk_norm_rope_fwd`` (fa_qk_norm_rope_bwd): from the gradients of its outputs returns
     (dq, dk, dq_weight, dk_weight); the last two are None without gains.  ``workspace``: a uint8 tensor of
     fa_qk_norm_rope_workspace_size bytes, to avoid the allocation."""
-    checked = _rope_check(q, k, cos, sin, q_weight, k_weight, positions)
-    for g, x, name in ((dq_out, q, "dq_out"), (dk_out, k, "dk_out")):
-        if g.shape != x.shape or g.dtype != x.dtype or g.device != x.device:
-            raise ValueError(f"{name} must have the shape, dtype and device of its output")
-    if workspace is not None and (workspace.device != q.device or not workspace.is_contiguous()):
-        raise ValueError("workspace must be contiguous, on the device of q")
-    if _elsewhere(checked[0], stream):
-        return _reenter(q.device, stream, lambda: _rope_bwd(checked, q, k, cos, sin, dq_out, dk_out, q_weight, k_weight,
-                                                            positions, eps, interleaved, workspace))
-    return _rope_bwd(checked, q, k, cos, sin, dq_out, dk_out, q_weight, k_weight, positions, eps, interleaved, workspace)
-
-
-def _rope_bwd(checked, q, k, cos, sin, dq_out, dk_out, q_weight, k_weight, positions, eps, interleaved, workspace):
-    """qk_norm_rope_bwd on tensors that _rope_check has seen, on the current device and stream."""
-    index, B, N, H, Hkv, d, rows, dt, wdt = checked
-    dq = torch.empty_like(q, memory_format=torch.contiguous_format)
-    dk = torch.empty_like(k, memory_format=torch.contiguous_format)
-    dwq = dwk = ws = None
-    size = 0
-    if q_weight is not None:
-        dwq, dwk = torch.empty_like(q_weight), torch.empty_like(k_weight)
-        ws = workspace
-        if ws is None:
-            size = lib().fa_qk_norm_rope_workspace_size(d)
-            ws = _empty((size,), (1,), torch.uint8, q.device)
-        else:
-            size = ws.numel() * ws.element_size()
-    rc = lib().fa_qk_norm_rope_bwd(q.data_ptr(), k.data_ptr(), _ptr(q_weight), _ptr(k_weight), cos.data_ptr(),
-                                   sin.data_ptr(), _ptr(positions), dq_out.data_ptr(), dk_out.data_ptr(),
-                                   dq.data_ptr(), dk.data_ptr(), _ptr(dwq), _ptr(dwk), B, N, H, Hkv, d,
-                                   _strides(q, "q"), _strides(k, "k"), _strides(dq_out, "dq_out"),
-                                   _strides(dk_out, "dk_out"), rows, eps, 1 if interleaved else 0, dt, wdt, _ptr(ws),
-                                   size, _current_handle(index))
-    if rc != 0:
-        raise FAError(rc, "fa_qk_norm_rope_bwd")
-    return dq, dk, dwq, dwk
-
-
-def _readable(g):
-    """An incoming gradient as the kernels read it: features contiguous, 16-byte strides and base."""
-    if g.is_contiguous() and g.data_ptr() % 16 == 0:
-        return g
-    unit = 16 // g.element_size()
-    sb, sn, sh, sd = g.stride()
-    if sd == 1 and sb % unit == 0 and sn % unit == 0 and sh % unit == 0 and g.data_ptr() % 16 == 0:
-        return g
-    return g.clone(memory_format=torch.contiguous_format)
-
-
-class _QKNormRope(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
-        ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
-        ctx.checked = _rope_check(q, k, cos, sin, q_weight, k_weight, positions)
-        ctx.eps, ctx.interleaved = eps, interleaved
-        if _elsewhere(ctx.checked[0], None):
-            return qk_norm_rope_fwd(q, k, cos, sin, q_weight, k_weight, positions, eps, interleaved)
-        return _rope_fwd(ctx.checked, q, k, cos, sin, q_weight, k_weight, positions, eps, interleaved)
-
-    @staticmethod
-    @torch.autograd.function.once_differentiable
-    def backward(ctx, dq_out, dk_out):
-        # autograd runs this on the forward's device and stream, with gradients of the outputs' shapes and dtype
-        q, k, q_weight, k_weight, cos, sin, positions = ctx.saved_tensors
-        dq, dk, dwq, dwk = _rope_bwd(ctx.checked, q, k, cos, sin, _readable(dq_out), _readable(dk_out), q_weight,
-                                     k_weight, positions, ctx.eps, ctx.interleaved, None)
-        return dq, dk, dwq, dwk, None, None, None, None, None
-
-
-def qk_norm_rope(q, k, cos, sin, q_weight=None, k_weight=None, positions=None, eps: float = 1e-6,
-                 interleaved: bool = False):
-    """Differentiable ``qk_norm_rope_fwd`` (gradients of q, k and the gains; the tables get none): the step before
-    ``attention``.  As with any autograd function, capture its backward into a CUDA graph only while no eager graph of
-    the same leaves is alive (PyTorch accumulates into a leaf on the stream of the graph that saw it first)."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k, q_weight, k_weight)):
-        return _QKNormRope.apply(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
-    return qk_norm_rope_fwd(q, k, cos, sin, q_weight, k_weight, positions, eps, interleaved)
-
-
-_CODES = (torch.float8_e4m3fn, torch.uint8)
-_SCALES = (torch.uint8, torch.float8_e8m0fnu)
-
-
-def _cache_check(k_cache, v_cache, block_table, lengths, kv_scale, what):
-    """(device index, fp8, num_pages, page_size, Hkv, d, B, max_pages) of a paged cache's checked tensors."""
-    shape, table_shape, dtype, index = k_cache.shape, block_table.shape, k_cache.dtype, k_cache.get_device()
-    if len(shape) != 4 or v_cache.shape != shape:
-        raise ValueError("k_cache and v_cache must be [num_pages, page_size, Hkv, d]")
-    fp8 = dtype in _CODES
-    if not fp8 and dtype != torch.bfloat16 or v_cache.dtype != dtype:
-        raise TypeError("k_cache and v_cache must both be bfloat16, or float8_e4m3fn (or its uint8 codes)")
-    num_pages, page_size, Hkv, d = shape
-    dense = k_cache.is_contiguous() and v_cache.is_contiguous() and block_table.is_contiguous() and lengths.is_contiguous()
-    same = v_cache.get_device() == index and block_table.get_device() == index and lengths.get_device() == index
-    if fp8:
-        if kv_scale is None:
-            raise ValueError("an 8-bit cache needs kv_scale [num_pages, Hkv, 2, page_size]")
-        if kv_scale.dtype not in _SCALES:
-            raise TypeError("kv_scale must be uint8 (or float8_e8m0fnu)")
-        if kv_scale.shape != (num_pages, Hkv, 2, page_size):
-            raise ValueError("kv_scale must be [num_pages, Hkv, 2, page_size]")
-        dense = dense and kv_scale.is_contiguous()
-        same = same and kv_scale.get_device() == index
-    elif kv_scale is not None:
-        raise ValueError("a bfloat16 cache takes no kv_scale")
-    if block_table.dtype != torch.int32 or lengths.dtype != torch.int32:
-        raise TypeError(f"block_table and {what} must be int32")
-    if len(table_shape) != 2 or lengths.shape != table_shape[:1]:
-        raise ValueError(f"block_table must be [B, max_pages] and {what} [B]")
-    if not dense:
-        raise ValueError("cache tensors must be contiguous")
-    if not same:
-        raise ValueError("all tensors must share one device")
-    if index < 0:
-        raise ValueError(_NO_CUDA)
-    return index, fp8, num_pages, page_size, Hkv, d, table_shape[0], table_shape[1]
+    args = (q, k, cos, sin, q_weight, k_weight, positions, eps, interleaved, dq_out, dk_out, workspace)
+    call = _native().norm_rope_bwd
+    return call(*args) if stream is None else _on_stream(q, stream, call, *args)
 
 
 def cache_append(k, v, k_cache, v_cache, block_table, start, kv_scale=None, count=None, stream=None):
@@ -831,62 +631,32 @@ def cache_append(k, v, k_cache, v_cache, block_table, start, kv_scale=None, coun
     (or float8_e8m0fnu), a power-of-two scale per row.  block_table [B, max_pages],
     start [B] and the optional count [B] (rows of each sequence, None: N) are int32.
     """
-    index, fp8, num_pages, page_size, Hkv, d, B, max_pages = _cache_check(k_cache, v_cache, block_table, start, kv_scale,
-                                                                          "start")
-    shape = k.shape
-    if len(shape) != 4 or v.shape != shape or shape[0] != B or shape[2] != Hkv or shape[3] != d:
-        raise ValueError("k and v must be [B, N, Hkv, d] for the cache's Hkv and d and block_table's B")
-    if k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
-        raise TypeError("k and v must be bfloat16")
-    if k.get_device() != index or v.get_device() != index:
-        raise ValueError("all tensors must share one device")
-    if count is not None:
-        if count.dtype != torch.int32:
-            raise TypeError("count must be int32")
-        if count.shape != start.shape or not count.is_contiguous() or count.get_device() != index:
-            raise ValueError("count must be a contiguous [B] tensor on the cache's device")
-    if _elsewhere(index, stream):
-        return _reenter(k.device, stream, lambda: cache_append(k, v, k_cache, v_cache, block_table, start, kv_scale, count))
-    rc = lib().fa_cache_append(k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(kv_scale),
-                               block_table.data_ptr(), start.data_ptr(), _ptr(count), B, shape[1], Hkv, d,
-                               _strides(k, "k"), _strides(v, "v"), page_size, num_pages, max_pages, 1 if fp8 else 0,
-                               _current_handle(index))
-    if rc != 0:
-        raise FAError(rc, "fa_cache_append")
+    args = (k, v, k_cache, v_cache, kv_scale, block_table, start, count)
+    call = _native().cache_append
+    return call(*args) if stream is None else _on_stream(k_cache, stream, call, *args)
 
 
 def cache_read(k_cache, v_cache, block_table, seqlens, length: int, kv_scale=None, k_out=None, v_out=None,
                stream=None):
     """The first ``length`` positions of every sequence out of a paged cache (fa_cache_read): returns
     (k, v) [B, length, Hkv, d] bf16, zeros at and past seqlens[b].  Cache tensors as in ``cache_append``."""
-    index, fp8, num_pages, page_size, Hkv, d, B, max_pages = _cache_check(k_cache, v_cache, block_table, seqlens,
-                                                                          kv_scale, "seqlens")
-    N, device = int(length), k_cache.device
-    if N < 0:
-        raise ValueError("length must be >= 0")
-    if k_out is not None:
-        _check_out(k_out, (B, N, Hkv, d), torch.bfloat16, device, "k_out")
-    if v_out is not None:
-        _check_out(v_out, (B, N, Hkv, d), torch.bfloat16, device, "v_out")
-    if _elsewhere(index, stream):
-        return _reenter(device, stream, lambda: cache_read(k_cache, v_cache, block_table, seqlens, N, kv_scale, k_out,
-                                                           v_out))
-    shape, strides = (B, N, Hkv, d), (N * Hkv * d, Hkv * d, d, 1)
-    k = _empty(shape, strides, torch.bfloat16, device) if k_out is None else k_out
-    v = _empty(shape, strides, torch.bfloat16, device) if v_out is None else v_out
-    rc = lib().fa_cache_read(k_cache.data_ptr(), v_cache.data_ptr(), _ptr(kv_scale), block_table.data_ptr(),
-                             seqlens.data_ptr(), k.data_ptr(), v.data_ptr(), B, N, Hkv, d, page_size, num_pages,
-                             max_pages, 1 if fp8 else 0, _current_handle(index))
-    if rc != 0:
-        raise FAError(rc, "fa_cache_read")
-    return k, v
+    args = (k_cache, v_cache, kv_scale, block_table, seqlens, length, k_out, v_out)
+    call = _native().cache_read
+    return call(*args) if stream is None else _on_stream(k_cache, stream, call, *args)
 
 
 def decode_fp8_workspace_size(B: int, H: int, Hkv: int, d: int, page_size: int, max_pages: int,
                               window_left: int | None = None) -> int:
     """Workspace bytes with which ``decode_paged_fp8`` splits long sequences as it would unconstrained."""
-    return int(lib().fa_decode_fp8_workspace_size(B, H, Hkv, d, page_size, max_pages,
-                                                  -1 if window_left is None else int(window_left)))
+    return int(lib().fa_decode_fp8_workspace_size(B, H, Hkv, d, page_size, max_pages, _window_left(window_left)))
+
+
+def _window_left(window_left):
+    if window_left is None:
+        return -1
+    if int(window_left) != window_left or window_left < 0:
+        raise ValueError("window_left must be None or an integer >= 0")
+    return min(int(window_left), 1 << 30)  # longer than every sequence
 
 
 def decode_paged_fp8(q, k_cache, v_cache, kv_scale, block_table, seqlens, scale: float | None = None,
@@ -898,45 +668,6 @@ def decode_paged_fp8(q, k_cache, v_cache, kv_scale, block_table, seqlens, scale:
     ``workspace`` (uint8 cuda tensor) defaults to a fresh buffer of
     ``decode_fp8_workspace_size`` bytes.
     """
-    if k_cache.dtype not in _CODES:
-        raise TypeError("decode_paged_fp8 takes an 8-bit cache (decode_paged: bfloat16)")
-    index, _, num_pages, page_size, Hkv, d, B, max_pages = _cache_check(k_cache, v_cache, block_table, seqlens, kv_scale,
-                                                                        "seqlens")
-    shape, device = q.shape, q.device
-    if len(shape) != 3 or shape[0] != B or shape[2] != d:
-        raise ValueError("q must be [B, H, d] for block_table's B and the cache's d")
-    if q.dtype != torch.bfloat16:
-        raise TypeError("q must be bfloat16")
-    if q.get_device() != index or not q.is_contiguous():
-        raise ValueError("q must be contiguous, on the cache's device")
-    H, w = shape[1], -1
-    if window_left is not None:
-        w = int(window_left)
-        if w != window_left or w < 0:
-            raise ValueError("window_left must be None or an integer >= 0")
-        w = min(w, 1 << 30)
-    if out is not None:
-        _check_out(out, (B, H, d), torch.bfloat16, device, "out")
-    if lse is not None:
-        _check_out(lse, (B, H), torch.float32, device, "lse")
-    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
-        raise ValueError("workspace must be contiguous, on the device of q")
-    if _elsewhere(index, stream):
-        return _reenter(device, stream, lambda: decode_paged_fp8(q, k_cache, v_cache, kv_scale, block_table, seqlens,
-                                                                 scale, window_left, out, lse, workspace))
-    o = torch.empty_like(q) if out is None else out
-    l = _empty((B, H), (H, 1), torch.float32, device) if lse is None else lse
-    ws = workspace
-    if ws is None:
-        size = lib().fa_decode_fp8_workspace_size(B, H, Hkv, d, page_size, max_pages, w)
-        if size:
-            ws = _empty((size,), (1,), torch.uint8, device)
-    else:
-        size = ws.numel() * ws.element_size()
-    rc = lib().fa_decode_paged_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), kv_scale.data_ptr(),
-                                   block_table.data_ptr(), seqlens.data_ptr(), o.data_ptr(), l.data_ptr(), B, H, Hkv, d,
-                                   page_size, num_pages, max_pages, _scale(scale, d), w, _ptr(ws), size,
-                                   _current_handle(index))
-    if rc != 0:
-        raise FAError(rc, "fa_decode_paged_fp8")
-    return o, l
+    args = (q, k_cache, v_cache, kv_scale, block_table, seqlens, scale, _window_left(window_left), out, lse, workspace)
+    call = _native().decode_paged_fp8
+    return call(*args) if stream is None else _on_stream(q, stream, call, *args)

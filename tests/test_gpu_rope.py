@@ -284,6 +284,30 @@ def test_empty_problems():
 
 
 @pytest.mark.gpu
+def test_strides_that_the_kernels_cannot_read_are_refused():
+    need_gpu()
+    q, k, cos, sin, w, _, gq, gk = _case(BF, 2, 3, 4, 2, 64, True, False, False, False, BF, seed=22)
+    wide = torch.zeros(2, 3, 4, 128, dtype=BF, device="cuda")[..., ::2]
+    with pytest.raises(ValueError, match="contiguous"):
+        fa.qk_norm_rope(wide, k, cos, sin)
+    odd = torch.zeros(2, 3, 4, 68, dtype=BF, device="cuda")[..., :64]
+    with pytest.raises(ValueError, match="16 bytes"):
+        fa.qk_norm_rope(odd, k, cos, sin)
+    with pytest.raises(ValueError, match="16 bytes"):
+        fa.qk_norm_rope_bwd(q, k, cos, sin, odd, gk)
+    with pytest.raises(fa.FAError) as e:                   # base not 16-byte aligned
+        fa.qk_norm_rope(torch.zeros(q.numel() + 1, dtype=BF, device="cuda")[1:].view(q.shape), k, cos, sin)
+    assert e.value.status == -3
+    with pytest.raises(ValueError, match="q_out"):
+        fa.qk_norm_rope_fwd(q, k, cos, sin, q_out=q.float())
+    # what they can: heads and positions in another order, one row for all (stride 0)
+    t = q.transpose(1, 2).contiguous().transpose(1, 2)
+    assert not t.is_contiguous() and torch.equal(fa.qk_norm_rope(t, k, cos, sin, *w)[0], fa.qk_norm_rope(q, k, cos, sin, *w)[0])
+    e = q[:, :, :1].expand(2, 3, 4, 64)
+    assert torch.equal(fa.qk_norm_rope(e, k, cos, sin, *w)[0], fa.qk_norm_rope(e.contiguous(), k, cos, sin, *w)[0])
+
+
+@pytest.mark.gpu
 def test_nan_and_inf_stay_in_their_rows():
     need_gpu()
     q, k, cos, sin, w, _, _, _ = _case(BF, 1, 4, 8, 2, 128, True, False, False, False, BF, seed=19)
