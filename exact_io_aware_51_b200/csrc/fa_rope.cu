@@ -20,6 +20,10 @@
 // takes the heads of one position, so the angles and gains are read once for
 // all of them.  All arithmetic is fp32 (packed pairs), each output is rounded
 // once.
+//
+// Measured on a B200 (GPU time), bf16, d = 128: forward B1 N16384 H32 + 32 (537 MB) 85
+// us, 6.3 TB/s; B1 N4096 H64 + 8 out of a packed projection (151 MB) 28 us, 5.4 TB/s;
+// backward B1 N16384 H32 + 32 (805 MB) 138 us with the gains' sums, 5.8 TB/s.
 #include <cuda_bf16.h>
 
 #include "fa_internal.h"

@@ -436,9 +436,9 @@ int fa_cache_read(const void* K_cache, const void* V_cache, const void* kv_scale
  *                last position) sees itself and the window_left positions before it, and
  *                pages wholly before those are neither looked up nor loaded.
  *   workspace    as fa_decode_paged, with fa_decode_fp8_workspace_size() bytes.
- * A row whose scale byte is 255 makes the heads that see it NaN.  The codes 0x7f and
- * 0xff, which fa_cache_append writes only in such rows, count as +-480 in a row with
- * another scale byte.  Out-of-range lengths and page indices leave the sequence's rows
+ * A row whose scale byte is 255 makes the heads that see it NaN; so does a NaN code (0x7f,
+ * 0xff) of K, and one of V its feature.  What hidden positions hold is of no effect.
+ * Out-of-range lengths and page indices leave the sequence's rows
  * empty (O = 0, LSE = -inf) and are reported, as in fa_decode_paged.
  *   max_pages * page_size <= 2^30, B * max_pages * page_size <= 2^37; the other limits as
  *   fa_decode_paged.

@@ -174,6 +174,18 @@ def test_nan_rows_reach_the_heads_that_see_them():
         assert torch.isfinite(o.float()).all() and torch.isfinite(lse).all()
         o, _ = _run((q, kc, vc, s2, table, sl), window_left=300 - 1 - 88)
         assert torch.isfinite(o.float()).all()
+    # a NaN code of K makes the heads NaN, one of V its feature; behind the end neither does
+    for cache, hit in ((0, slice(None)), (1, slice(37, 38))):
+        pools = [kc.clone(), vc.clone()]
+        pools[cache][int(table[1, 5]), 7, 1, 37] = 0xFF
+        o, _ = _run((q, *pools, sc, table, sl))
+        assert torch.isnan(o[1, 4:, hit].float()).all()
+        if cache == 1:
+            rest = [f for f in range(128) if f != 37]
+            assert torch.equal(o[1, 4:][:, rest], clean[0][1, 4:][:, rest])
+        assert torch.equal(o[0], clean[0][0]) and torch.equal(o[1, :4], clean[0][1, :4])
+        o, _ = _run((q, *pools, sc, table, short))
+        assert torch.isfinite(o.float()).all()
     # a query of NaN, and one of Inf
     for bad in (float("nan"), float("inf")):
         q2 = q.clone()
