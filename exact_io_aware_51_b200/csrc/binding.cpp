@@ -388,6 +388,12 @@ int64_t integer(PyObject* o) {
   return v;
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v == 1;
+}
+
 PyObject* pack(const Tensor* t, Py_ssize_t n) {
   PyObject* r = PyTuple_New(n);
   if (!r) throw python_error();
@@ -427,7 +433,7 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F&& f) {
 
 Rope rope_of(PyObject* const* a) {  // q, k, cos, sin, q_weight, k_weight, positions, eps, interleaved
   return Rope{tensor(a[0]), tensor(a[1]), tensor(a[2]), tensor(a[3]), maybe(a[4]),
-              maybe(a[5]),  maybe(a[6]),  number(a[7]), PyObject_IsTrue(a[8]) == 1};
+              maybe(a[5]),  maybe(a[6]),  number(a[7]), truth(a[8])};
 }
 
 PyObject* py_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {  // rope_of, with autograd

@@ -246,6 +246,53 @@ def test_table_entries_past_the_end_are_not_read():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("fp8,d", [(True, 128), (True, 64), (False, 128)])
+def test_large_append(fp8, d):
+    """Enough rows that a warp takes several groups of positions: sampled rows against the oracle, all other rows of
+    the pools as they were, and the rows read back against the rows given."""
+    need_gpu()
+    B, N, Hkv, page = 8, 4096, 8, 16
+    g = torch.Generator().manual_seed(36)
+    starts = torch.randint(0, 50, (B,), generator=g).tolist()
+    counts = [0, 1, N, N - 1, 5, 17, 2048, 3000]
+    table, pages = _table([s + c for s, c in zip(starts, counts)], page, 3, 3, g)
+    kc, vc, sc = _pool(pages, page, Hkv, d, fp8, g)
+    k, v = _rows((B, N, Hkv, d), g), _rows((B, N, Hkv, d), g)
+    gk, gv, gs = kc.cuda(), vc.cuda(), _c(sc)
+    start, count = (torch.tensor(x, dtype=torch.int32) for x in (starts, counts))
+    fa.cache_append(k.cuda(), v.cuda(), gk, gv, table.cuda(), start.cuda(), kv_scale=gs, count=count.cuda())
+    assert fa.last_device_status()[0] == 0
+    gk, gv, gs = gk.cpu(), gv.cpu(), None if gs is None else gs.cpu()
+    written = torch.zeros((pages, page), dtype=torch.bool)
+    for b in range(B):
+        at = torch.arange(starts[b], starts[b] + counts[b])
+        written[table[b, at // page].long(), at % page] = True
+    assert torch.equal(gk[~written], kc[~written]) and torch.equal(gv[~written], vc[~written])
+    if fp8:
+        keep = ~written[:, None, None, :].expand(pages, Hkv, 2, page)
+        assert torch.equal(gs[keep], sc[keep])
+    for b in range(B):
+        for n in {0, 1, counts[b] // 2, counts[b] - 9, counts[b] - 2, counts[b] - 1}:
+            if not 0 <= n < counts[b]:
+                continue
+            pg, slot = int(table[b, (starts[b] + n) // page]), (starts[b] + n) % page
+            for which, (x, pool) in enumerate(((k, gk), (v, gv))):
+                if fp8:
+                    codes, byte = S.quantise_rows(x[b, n].double())
+                    assert np.array_equal(pool[pg, slot].numpy(), codes)
+                    assert np.array_equal(gs[pg, :, which, slot].numpy(), byte)
+                else:
+                    assert torch.equal(pool[pg, slot], x[b, n])
+    out = fa.cache_read(gk.cuda(), gv.cuda(), table.cuda(), (start + count).cuda(), N + 50, kv_scale=_c(gs))
+    for x, y in zip((k, v), out):
+        for b in range(B):
+            got = y[b, starts[b]:starts[b] + counts[b]].cpu().float()
+            ref = x[b, :counts[b]].float()
+            top = ref.abs().amax(-1, keepdim=True)  # a code is off by 2^-4 of itself, or half the smallest step: 2^-10 of 448ths
+            assert bool(((got - ref).abs() <= (torch.maximum(ref.abs() * 2.0 ** -4, top * 2.0 ** -17) if fp8 else 0 * top)).all())
+
+
+@pytest.mark.gpu
 def test_pools_beyond_32_bit_offsets():
     """Pools of 5 GB each (K, V), the sequences' pages at their far end: append, read and decode."""
     need_gpu()

@@ -281,6 +281,18 @@ def test_many_sequences_share_the_ranges(d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H,Hkv,d", [(6, 2, 128), (24, 2, 64)])
+def test_a_batch_of_short_sequences_runs_whole(H, Hkv, d):
+    need_gpu()
+    g = torch.Generator().manual_seed(16)
+    lens = torch.randint(0, 385, (150,), generator=g).tolist()
+    args = _make(150, H, Hkv, d, 32, lens, seed=16, max_pages=12)
+    assert fa.decode_fp8_workspace_size(150, H, Hkv, d, 32, 12) == 0
+    o, lse = _run(args, scale=0.1)
+    _check(args, o, lse, 0.1)
+
+
+@pytest.mark.gpu
 def test_given_outputs_and_their_checks():
     need_gpu()
     args = [t.cuda() for t in _make(2, 4, 2, 64, 8, [30, 9], seed=14)]

@@ -64,6 +64,7 @@ CASES = [
     (F32, 1, 50, 7, 2, 128, True, False, True, True, F32),
     (F32, 3, 21, 6, 3, 128, False, False, False, True, F32),
     (BF, 2, 19, 0, 3, 64, True, False, False, True, BF),       # keys alone
+    (F32, 2, 19, 3, 3, 64, True, False, False, True, BF),      # gains in fewer bits than the rows
 ]
 
 
@@ -147,6 +148,48 @@ def test_backward_of_many_rows_uses_every_block():
     qo, ko = fa.qk_norm_rope(q, k, cos, sin, w[0], w[1], pos)
     _check_fwd(q, w[0], cos, sin, pos, False, qo)
     _check_fwd(k, w[1], cos, sin, pos, False, ko)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,inter,d,norm", [(BF, False, 128, True), (BF, True, 64, True), (F32, False, 128, True),
+                                                (BF, False, 64, False)])
+def test_many_positions_and_heads(dtype, inter, d, norm):
+    """Enough warps that each takes eight groups of rows, with heads that do not fill the last group, q out of
+    a packed projection."""
+    need_gpu()
+    rows = 512 // d
+    case = (dtype, 1, 3301, 8 * rows + 1, rows + 1, d, norm, inter, True, True, F32)
+    q, k, cos, sin, w, pos, gq, gk = _case(*case, seed=23)
+    qo, ko = fa.qk_norm_rope(q, k, cos, sin, w[0], w[1], pos, interleaved=inter)
+    _check_fwd(q, w[0], cos, sin, pos, inter, qo)
+    _check_fwd(k, w[1], cos, sin, pos, inter, ko)
+    dq, dk, dwq, dwk = fa.qk_norm_rope_bwd(q, k, cos, sin, gq, gk, w[0], w[1], pos, interleaved=inter)
+    _check_bwd(q, w[0], cos, sin, pos, inter, gq, dq, dwq)
+    _check_bwd(k, w[1], cos, sin, pos, inter, gk, dk, dwk)
+
+
+@pytest.mark.gpu
+def test_tensors_beyond_32_bit_offsets():
+    """q and its output of 2.3e9 elements: the last positions are those of a small call."""
+    need_gpu()
+    N, H, d, last = 280000, 64, 128, 37
+    g = torch.Generator().manual_seed(24)
+    tail = torch.randn((1, last, H, d), generator=g).to(BF).cuda()
+    k = torch.randn((1, last, 1, d), generator=g).to(BF).cuda()
+    cos, sin = fa.rope_tables(N, d)
+    w = (1 + 0.3 * torch.randn(d, generator=g)).to(BF).cuda()
+    q = torch.zeros((1, N, H, d), dtype=BF, device="cuda")
+    kk = torch.zeros((1, N, 1, d), dtype=BF, device="cuda")
+    assert q.numel() > 2 ** 31
+    q[:, -last:], kk[:, -last:] = tail, k
+    pos = torch.arange(N - last, N, dtype=torch.int32, device="cuda").view(1, last)
+    want = fa.qk_norm_rope(tail, k, cos, sin, w, w, pos)
+    got = fa.qk_norm_rope(q, kk, cos, sin, w, w)
+    assert torch.equal(got[0][:, -last:], want[0]) and torch.equal(got[1][:, -last:], want[1])
+    assert torch.count_nonzero(got[0][:, :-last]) == 0
+    want = fa.qk_norm_rope_bwd(tail, k, cos, sin, tail, k, w, w, pos)
+    got = fa.qk_norm_rope_bwd(q, kk, cos, sin, q, kk, w, w)
+    assert torch.equal(got[0][:, -last:], want[0]) and torch.equal(got[1][:, -last:], want[1])
 
 
 @pytest.mark.gpu

@@ -260,6 +260,8 @@ def test_python_norm_rope_refusals(L):
         f(q, None, c, c)
     with pytest.raises(TypeError):
         f(q, k, c, c, eps="small")
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        f(q, k, c, c, interleaved=torch.ones(2))
 
 
 def test_python_cache_refusals(L):
