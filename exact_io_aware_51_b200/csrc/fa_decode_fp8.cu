@@ -37,15 +37,17 @@
 // d = 128, 16-token pages, 632 MB: 101 us, 6.25 TB/s (95% of a copy's 6.57); one
 // sequence of 100000, 206 MB: 40 us, of which 8 us are the start, the last merge and the
 // join.  Beyond 8 heads a K/V head, and for d = 64, the consumers' latency and not the
-// memory bounds it (64 heads on 4: 77 us for 290 MB).  What did not pay:
+// memory bounds it (64 heads on 4: 67 us for 290 MB; with Q's fragments in registers the
+// two blocks of positions had to go one after the other: 77 us).  What did not pay:
 //   * a grid of (sequence, chunk) with two CTAs per SM, codes converted with integer
 //     shifts (7 operations a word): 161 us;
 //   * e4m3 operands for S^T with m16n8k32 and q split in two: 129 us (the instruction is
 //     converted and multiplied as f16 on this GPU, at four times the instructions);
 //   * S^T on tcgen05 into tensor memory, a lane per position for the softmax: 108 us, 7.5
-//     instead of 6.4 us for a short sequence and 117 instead of 77 us at 16 heads a K/V
+//     instead of 6.4 us for a short sequence, 28.3 instead of 27.5 us for one head a K/V
 //     head: the product's round trip through barriers and tensor memory costs a tile
 //     more than the conversions of K do;
+//   * three CTAs per SM with more than 8 heads a K/V head: spilled registers, 122 us;
 //   * two accumulator chains for S^T: the same time.
 //
 // A row whose scale byte is 255 (NaN) makes the heads that see it NaN.  A
@@ -77,7 +79,7 @@ struct Cfg8 {
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kCtas = NT == 2 ? 2 : D == 128 ? 3 : 4;   // per SM
   static constexpr int kStages = NT == 2 ? (D == 128 ? 3 : 4) : (D == 128 ? 2 : 3);
-  static constexpr int kBlocks = NT == 1 ? 2 : 1;                // blocks of 16 positions that a warp takes at a time (registers)
+  static constexpr bool kSharedQ = NT == 2;                      // Q's fragments in shared memory (registers)
   static constexpr int kRounds = NT == 1 ? 2 : D / 32;                  // the merge goes through in slices of the features
   static constexpr int kSlice = D / kRounds;
   static constexpr int kORow = kSlice + 4;
@@ -88,6 +90,7 @@ struct Cfg8 {
   static constexpr int kSmemBytes = kOffBar + kBarBytes;
   static_assert(kCtas * (kSmemBytes + 1024) <= 227 * 1024, "CTAs per SM");
   static_assert(kStages <= 4, "barrier block");
+  static_assert(!kSharedQ || NT * (D / 16) * 256 <= kConsumers * 8 * NT * kORow * 4, "Q fits in the merge's place");
 };
 
 struct Bars8 {
@@ -423,7 +426,8 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
     const int kbeg = walk.s.base + walk.off * kTileKeys;
     // Q as the B operand: head nt * 8 + g, the features in the order in which a lane holds a K row
     // (its 16-byte units t4 and, for d = 128, t4 + 4): q = (qh + ql / 16) 2^(e - 134)
-    uint32_t qb[NT][D / 16][2];
+    uint32_t qb[NT][D / 16][2];  // kSharedQ: on their way to the merge's place, [nt][k step][lane]
+    const uint32_t q_at = smem_u32(smem + C::kOffMerge) + lane * 8;
     float qf[NT][2];  // heads 2 t4, 2 t4 + 1: scale_log2 * 2^(e - 134)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -462,6 +466,17 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
       }
     }
     // scores are held as t = <q, k> with q's power of two still in it: x = t qf
+    if constexpr (C::kSharedQ) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          if ((k & 3) == warp)
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(q_at + (nt * (D / 16) + k) * 256), "r"(qb[nt][k][0]),
+                         "r"(qb[nt][k][1])
+                         : "memory");
+      sync_consumers();
+    }
     float o[D / 16][NT][4];
     float mt[NT][2], mq[NT][2], lazy[NT][2];  // reference in t; mq = reference in x (0 while there is none)
     float2 l[NT];
@@ -511,18 +526,16 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
         }
         __syncwarp();
       }
-#pragma unroll 1
-      for (int u0 = 0; u0 < 2; u0 += C::kBlocks) {
       // S^T = K Q^T
-      float s[C::kBlocks][NT][4];
+      float s[2][NT][4];
 #pragma unroll
-      for (int u = 0; u < C::kBlocks; ++u) {
+      for (int u = 0; u < 2; ++u) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) s[u][nt][0] = s[u][nt][1] = s[u][nt][2] = s[u][nt][3] = 0.f;
 #pragma unroll
         for (int q = 0; q < D / 64; ++q) {
-          const uint4 ra = lds128(ks + unit_off<D>((u0 + u) * 16 + kg, t4 + 4 * q));
-          const uint4 rb = lds128(ks + unit_off<D>((u0 + u) * 16 + 8 + kg, t4 + 4 * q));
+          const uint4 ra = lds128(ks + unit_off<D>(u * 16 + kg, t4 + 4 * q));
+          const uint4 rb = lds128(ks + unit_off<D>(u * 16 + 8 + kg, t4 + 4 * q));
           const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -530,12 +543,17 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
             f16_halves(wa[k], a0, a2);
             f16_halves(wb[k], a1, a3);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(s[u][nt], a0, a1, a2, a3, qb[nt][4 * q + k][0], qb[nt][4 * q + k][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              uint32_t b0 = qb[nt][4 * q + k][0], b1 = qb[nt][4 * q + k][1];
+              if constexpr (C::kSharedQ)
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(b0), "=r"(b1) : "r"(q_at + (nt * (D / 16) + 4 * q + k) * 256));
+              mma_f16(s[u][nt], a0, a1, a2, a3, b0, b1);
+            }
           }
         }
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          const float f = __shfl_sync(0xffffffffu, kf, (u0 + u) * 16 + hh * 8 + kg);
+          const float f = __shfl_sync(0xffffffffu, kf, u * 16 + hh * 8 + kg);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -544,10 +562,10 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
       }
       if (edge) {
 #pragma unroll
-        for (int u = 0; u < C::kBlocks; ++u)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
-            const int key = key0 + warp * kWarpKeys + (u0 + u) * 16 + hh * 8 + kg;
+            const int key = key0 + warp * kWarpKeys + u * 16 + hh * 8 + kg;
             if (key >= kend || key < lo) {
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) s[u][nt][2 * hh] = s[u][nt][2 * hh + 1] = -INFINITY;
@@ -560,8 +578,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          mx[nt][i] = fmaxf(s[0][nt][i], s[0][nt][2 + i]);
-          if constexpr (C::kBlocks == 2) mx[nt][i] = fmaxf(mx[nt][i], fmaxf(s[1][nt][i], s[1][nt][2 + i]));
+          mx[nt][i] = fmaxf(fmaxf(s[0][nt][i], s[0][nt][2 + i]), fmaxf(s[1][nt][i], s[1][nt][2 + i]));
           grow |= mx[nt][i] > mt[nt][i] + lazy[nt][i];
         }
       if (__any_sync(0xffffffffu, grow)) {
@@ -592,12 +609,12 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
       }
       // P^T as the B operand: p * 2^(V byte - eref) * 2^kPShift in f16, transposed
       const float vf = __uint_as_float(static_cast<uint32_t>(max(0, vbyte - eref + 127 + kPShift)) << 23);
-      uint32_t pb[C::kBlocks][NT][2];
+      uint32_t pb[2][NT][2];
 #pragma unroll
-      for (int u = 0; u < C::kBlocks; ++u)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-          const float f = __shfl_sync(0xffffffffu, vf, (u0 + u) * 16 + hh * 8 + kg);
+          const float f = __shfl_sync(0xffffffffu, vf, u * 16 + hh * 8 + kg);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const float2 p = make_float2(ex2(fmaf(s[u][nt][2 * hh], qf[nt][0], -mq[nt][0])),
@@ -609,11 +626,11 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
         }
       // O^T += V^T P^T: one ldmatrix.trans covers 16 positions x 32 features
 #pragma unroll
-      for (int u = 0; u < C::kBlocks; ++u)
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t r[4];
-          ldsm_x4_t(vs + unit_off<D>((u0 + u) * 16 + (mi & 1) * 8 + key_of<D>(rr), 2 * cc + (mi >> 1)), r);
+          ldsm_x4_t(vs + unit_off<D>(u * 16 + (mi & 1) * 8 + key_of<D>(rr), 2 * cc + (mi >> 1)), r);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             uint32_t a0, a1, a2, a3;
@@ -623,7 +640,6 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
             for (int nt = 0; nt < NT; ++nt) mma_f16(o[2 * cc + i][nt], a0, a1, a2, a3, pb[u][nt][0], pb[u][nt][1]);
           }
         }
-      }
       if (edge) fence_proxy_async_smem();  // the next TMA write of the stage follows the zeros
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->empty[st]);
