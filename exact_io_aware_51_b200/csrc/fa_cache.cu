@@ -89,6 +89,7 @@ __device__ __forceinline__ uint32_t codes4(uint32_t lo, uint32_t hi, float inv) 
 
 template <int D, bool kFp8>
 __global__ void __launch_bounds__(kWarps * 32) cache_append_kernel(const CacheArgs a) {
+  wait_for_previous_kernel();
   Unit u;
   if (!unit_of<D>(a, u)) return;
   const int sub = lane_id() % (D / 16);
@@ -165,6 +166,7 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
 
 template <int D, bool kFp8>
 __global__ void __launch_bounds__(kWarps * 32) cache_read_kernel(const CacheArgs a) {
+  wait_for_previous_kernel();
   Unit u;
   if (!unit_of<D>(a, u)) return;
   const int sub = lane_id() % (D / 16);
@@ -220,11 +222,9 @@ __global__ void __launch_bounds__(kWarps * 32) cache_read_kernel(const CacheArgs
 template <int D>
 cudaError_t launch_d(const CacheArgs& a, bool fp8, bool append, cudaStream_t s) {
   const unsigned int blocks = (a.units + kWarps - 1) / kWarps;
-  if (append && fp8) cache_append_kernel<D, true><<<blocks, kWarps * 32, 0, s>>>(a);
-  else if (append) cache_append_kernel<D, false><<<blocks, kWarps * 32, 0, s>>>(a);
-  else if (fp8) cache_read_kernel<D, true><<<blocks, kWarps * 32, 0, s>>>(a);
-  else cache_read_kernel<D, false><<<blocks, kWarps * 32, 0, s>>>(a);
-  return cudaGetLastError();
+  const dim3 grid(blocks), block(kWarps * 32);
+  if (append) return launch_behind(fp8 ? cache_append_kernel<D, true> : cache_append_kernel<D, false>, grid, block, 0, s, a);
+  return launch_behind(fp8 ? cache_read_kernel<D, true> : cache_read_kernel<D, false>, grid, block, 0, s, a);
 }
 
 }  // namespace

@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
+  wait_for_previous_kernel();
   // ---- where this CTA's range of tiles begins ----
   Walk walk;
   const int range = blockIdx.y;
@@ -762,7 +763,7 @@ __global__ void __launch_bounds__(128) decode_fp8_join_kernel(const Decode8Args 
   const int warp = warp_id(), lane = lane_id();
   __shared__ float s_max[4], s_w[4];
   __shared__ float s_acc[4][D];
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials of the kernel before
+  wait_for_previous_kernel();  // its partials
   const int4 at = a.borders[border];  // sequence at the border, tiles before it, its tiles, tiles per range
   const int b = at.x, begin = at.y, len = at.w;
   if (b < 0 || begin >= border * len || begin < (border - 1) * len) return;
@@ -858,18 +859,9 @@ cudaError_t launch_nt(const CUtensorMap& tk, const CUtensorMap& tv, const Decode
                                        C::kSmemBytes);
   if (e != cudaSuccess) return e;
   const dim3 grid(a.Hkv * a.hgroups, a.ranges ? a.ranges : a.B);
-  decode_fp8_kernel<D, NT><<<grid, kThreads, C::kSmemBytes, s>>>(tk, tv, a, c);
-  if ((e = cudaGetLastError()) != cudaSuccess || a.ranges < 2) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.H, a.ranges - 1);
-  cfg.blockDim = dim3(128);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its start overlaps the end of the kernel before
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_fp8_join_kernel<D>, a);
+  e = launch_behind(decode_fp8_kernel<D, NT>, grid, dim3(kThreads), C::kSmemBytes, s, tk, tv, a, c);
+  if (e != cudaSuccess || a.ranges < 2) return e;
+  return launch_behind(decode_fp8_join_kernel<D>, dim3(a.H, a.ranges - 1), dim3(128), 0, s, a);
 }
 
 }  // namespace

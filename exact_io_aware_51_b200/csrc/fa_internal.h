@@ -212,6 +212,26 @@ struct CacheArgs {
 };
 cudaError_t launch_cache(const CacheArgs& a, int d, bool fp8, bool append, cudaStream_t s);
 
+// Launch of a kernel that begins with griddepcontrol.wait: its blocks may be brought up while the
+// kernel before it on the stream ends, and wait there for that kernel's end and writes.
+template <typename... K, typename... A>
+cudaError_t launch_behind(void (*kernel)(K...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<K>(args)...);
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+#endif
+
 // Kernel launchers (each returns the cudaError_t of the launch).
 cudaError_t launch_fwd_bf16(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                             const CUtensorMap& to, const FwdArgs& a, const DevCtl& c, cudaStream_t s);

@@ -244,6 +244,7 @@ template <typename T, int D, bool kNorm, bool kInter, int kAhead>
 __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 && !kInter ? 5 : 4) rope_fwd_kernel(const RopeArgs a) {
   constexpr int kLanes = D / 16;
   constexpr int kRows = 32 / kLanes;
+  wait_for_previous_kernel();
   const int lane = lane_id();
   const int token = blockIdx.x * kWarps + warp_id();
   if (token >= a.tokens) return;
@@ -385,6 +386,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_bwd_kernel(const RopeArgs
   constexpr int kLanes = D / 16;
   constexpr int kRows = 32 / kLanes;
   constexpr int kStep = kWarps * 32 * 16;
+  wait_for_previous_kernel();
   const int lane = lane_id(), warp = warp_id();
   const int sub = lane % kLanes;
   const bool is_q = static_cast<int>(blockIdx.x) < a.q_blocks;
@@ -537,7 +539,7 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__
   const int lo = blockIdx.x ? q_blocks : 0, hi = blockIdx.x ? blocks : q_blocks;
   const float* p = partial + blockIdx.y * 32 + f;
   double v = 0.0;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the partial sums of the kernel before
+  wait_for_previous_kernel();  // its partial sums
 #pragma unroll 8
   for (int i = lo + part; i < hi; i += 32) v += static_cast<double>(__ldcg(p + static_cast<size_t>(i) * D));
   sums[f][part] = v;
@@ -556,21 +558,18 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__
 }
 
 template <typename T, int D, bool kNorm, bool kInter>
-void launch_fwd_k(const RopeArgs& a, cudaStream_t s) {
+cudaError_t launch_fwd_k(const RopeArgs& a, cudaStream_t s) {
   const dim3 grid((a.tokens + kWarps - 1) / kWarps, a.q_groups + a.k_groups);
   constexpr int kMany = sizeof(T) == 2 ? 4 : 2;  // registers
-  if (a.per >= 4) rope_fwd_kernel<T, D, kNorm, kInter, kMany><<<grid, kWarps * 32, 0, s>>>(a);
-  else rope_fwd_kernel<T, D, kNorm, kInter, kMany / 2><<<grid, kWarps * 32, 0, s>>>(a);
+  if (a.per >= 4) return launch_behind(rope_fwd_kernel<T, D, kNorm, kInter, kMany>, grid, dim3(kWarps * 32), 0, s, a);
+  return launch_behind(rope_fwd_kernel<T, D, kNorm, kInter, kMany / 2>, grid, dim3(kWarps * 32), 0, s, a);
 }
 
 template <typename T, int D>
 cudaError_t launch_fwd_d(const RopeArgs& a, cudaStream_t s) {
   const bool norm = a.q.w != nullptr;
-  if (norm && a.interleaved) launch_fwd_k<T, D, true, true>(a, s);
-  else if (norm) launch_fwd_k<T, D, true, false>(a, s);
-  else if (a.interleaved) launch_fwd_k<T, D, false, true>(a, s);
-  else launch_fwd_k<T, D, false, false>(a, s);
-  return cudaGetLastError();
+  if (norm) return a.interleaved ? launch_fwd_k<T, D, true, true>(a, s) : launch_fwd_k<T, D, true, false>(a, s);
+  return a.interleaved ? launch_fwd_k<T, D, false, true>(a, s) : launch_fwd_k<T, D, false, false>(a, s);
 }
 
 template <typename T, int D, bool kNorm, bool kInter>
@@ -579,8 +578,7 @@ cudaError_t launch_bwd_k(const RopeArgs& a, cudaStream_t s) {
   const cudaError_t e =
       cudaFuncSetAttribute(rope_bwd_kernel<T, D, kNorm, kInter>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (e != cudaSuccess) return e;
-  rope_bwd_kernel<T, D, kNorm, kInter><<<a.blocks, kWarps * 32, kBytes, s>>>(a);
-  return cudaGetLastError();
+  return launch_behind(rope_bwd_kernel<T, D, kNorm, kInter>, dim3(a.blocks), dim3(kWarps * 32), kBytes, s, a);
 }
 
 template <typename T, int D>
@@ -593,17 +591,8 @@ cudaError_t launch_bwd_d(const RopeArgs& a, cudaStream_t s) {
   else if (a.interleaved) e = launch_bwd_k<T, D, false, true>(a, s);
   else e = launch_bwd_k<T, D, false, false>(a, s);
   if (e != cudaSuccess || !norm) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2, D / 32);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its start overlaps the end of the kernel before
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, rope_dw_kernel<D>, static_cast<const float*>(a.partial), a.q_blocks, a.blocks, a.dwq,
-                            a.dwk, a.w_f32);
+  return launch_behind(rope_dw_kernel<D>, dim3(2, D / 32), dim3(1024), 0, s, a.partial, a.q_blocks, a.blocks, a.dwq, a.dwk,
+                       a.w_f32);
 }
 
 }  // namespace
