@@ -375,7 +375,8 @@ int fa_qk_norm_rope(const void* Q, const void* K, const void* q_weight, const vo
  * ([d] of weight_dtype; sums over all rows in a fixed order: the same call gives
  * the same bits).  The tables get no gradient.
  *   workspace    device buffer of fa_qk_norm_rope_workspace_size(d) bytes, 256-byte
- *                aligned, overwritten; not needed (NULL) without gains.
+ *                aligned, overwritten; not needed (NULL) without gains.  Calls that may run
+ *                at the same time need a buffer each.
  */
 int fa_qk_norm_rope_bwd(const void* Q, const void* K, const void* q_weight, const void* k_weight,
                         const float* cos_table, const float* sin_table, const int* positions, const void* dQ_out,
@@ -435,7 +436,9 @@ int fa_cache_read(const void* K_cache, const void* V_cache, const void* kv_scale
  *   window_left  -1: every cached position is visible; else the query (the sequence's
  *                last position) sees itself and the window_left positions before it, and
  *                pages wholly before those are neither looked up nor loaded.
- *   workspace    as fa_decode_paged, with fa_decode_fp8_workspace_size() bytes.
+ *   workspace    as fa_decode_paged, with fa_decode_fp8_workspace_size() bytes.  Calls that
+ *                may run at the same time (other streams, captured graphs replayed beside
+ *                one another) need a buffer each.
  * A row whose scale byte is 255 makes the heads that see it NaN; so does a NaN code (0x7f,
  * 0xff) of K, and one of V its feature.  What hidden positions hold is of no effect.
  * Out-of-range lengths and page indices leave the sequence's rows
