@@ -48,7 +48,8 @@
 //     head: the product's round trip through barriers and tensor memory costs a tile
 //     more than the conversions of K do;
 //   * three CTAs per SM with more than 8 heads a K/V head: spilled registers, 122 us;
-//   * two accumulator chains for S^T: the same time.
+//   * two accumulator chains for S^T: the same time; ranges cut to 32 positions instead
+//     of whole tiles: 1% slower (a tile that a border cuts is walked twice).
 //
 // A row whose scale byte is 255 (NaN) makes the heads that see it NaN.  A
 // sequence with no position gets O = 0, LSE = -inf, and so does one with a
