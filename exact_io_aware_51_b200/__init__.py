@@ -3,7 +3,8 @@
 This module only marshals arguments: it checks tensor shapes, dtypes and
 devices, allocates outputs with PyTorch (PyTorch is used for device memory and
 streams only), and calls the C ABI declared in ``include/fa.h`` through
-ctypes.  Every step of the computation runs in the library's CUDA kernels;
+ctypes; the operators around the attention (norm and rotation, cache rows, the
+8-bit decode), whose calls are short, do the same in ``csrc/binding.cpp``.  Every step of the computation runs in the library's CUDA kernels;
 there is no CPU fallback.  If the library is missing, every call raises.
 
     o, lse = fwd(q, k, v, causal=False)          # q, k, v: [B, N, H, d] cuda

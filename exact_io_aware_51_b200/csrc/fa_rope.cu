@@ -14,16 +14,19 @@
 // forward saves nothing.
 //
 // Both are bound by the bytes they move (x in, out; x, g in, dx out).  A lane
-// holds 16 features of a row: 8 from each half, so both elements of a pair are
-// in one thread in either layout, the loads and stores are 16 bytes wide, and
-// a row takes d / 16 lanes (a warp 4 rows of d = 128, 8 of d = 64).  A warp
-// takes the heads of one position, so the angles and gains are read once for
-// all of them.  All arithmetic is fp32 (packed pairs), each output is rounded
-// once.
+// holds 16 features of a row, the same 8 of each half, so both elements of a
+// pair are in one thread in either layout.  They come in runs of 16 bytes (two
+// of 8 bf16, four of 4 fp32), neighbouring lanes' runs next to one another, so
+// every access fills whole sectors.  A row takes d / 16 lanes (a warp 4 rows of
+// d = 128, 8 of d = 64).  A warp takes the heads of one position, so the angles
+// and gains are read once for all of them.  All arithmetic is fp32 (packed
+// pairs), each output is rounded once.
 //
-// Measured on a B200 (GPU time), bf16, d = 128: forward B1 N16384 H32 + 32 (537 MB) 85
+// Measured on a B200 (GPU time), d = 128, bf16: forward B1 N16384 H32 + 32 (537 MB) 85
 // us, 6.3 TB/s; B1 N4096 H64 + 8 out of a packed projection (151 MB) 28 us, 5.4 TB/s;
-// backward B1 N16384 H32 + 32 (805 MB) 138 us with the gains' sums, 5.8 TB/s.
+// backward B1 N16384 H32 + 32 (805 MB) 144 us with the gains' sums, 5.6 TB/s.
+// fp32: B2 N4096 H32 + 8 forward (335 MB) 61 us, 5.5 TB/s; backward (503 MB) 86 us, 5.9
+// TB/s (130 us with a lane's 8 features of a half side by side: 32-byte steps).
 #include <cuda_bf16.h>
 
 #include "fa_internal.h"
@@ -34,7 +37,7 @@ namespace {
 
 constexpr int kWarps = 4;
 
-// 16 features of one row: two runs of 8 (first half, second half)
+// 16 features of one row, in runs of 16 bytes
 template <typename T>
 struct Raw;
 template <>
@@ -46,6 +49,12 @@ struct Raw<float> {
   float4 a0, a1, b0, b1;
 };
 
+// The first feature of x[j], the lane's j-th pair of neighbouring features (j = 0..7)
+template <typename T, int D>
+__device__ __forceinline__ constexpr int feature(int j, int sub) {
+  return sizeof(T) == 2 ? (j >> 2) * (D / 2) + 8 * sub + 2 * (j & 3) : (j >> 1) * (D / 4) + 4 * sub + 2 * (j & 1);
+}
+
 template <int D>
 __device__ __forceinline__ void load_row(Raw<__nv_bfloat16>& r, const __nv_bfloat16* p, int sub) {
   r.a = *reinterpret_cast<const uint4*>(p + 8 * sub);
@@ -53,10 +62,10 @@ __device__ __forceinline__ void load_row(Raw<__nv_bfloat16>& r, const __nv_bfloa
 }
 template <int D>
 __device__ __forceinline__ void load_row(Raw<float>& r, const float* p, int sub) {
-  r.a0 = *reinterpret_cast<const float4*>(p + 8 * sub);
-  r.a1 = *reinterpret_cast<const float4*>(p + 8 * sub + 4);
-  r.b0 = *reinterpret_cast<const float4*>(p + D / 2 + 8 * sub);
-  r.b1 = *reinterpret_cast<const float4*>(p + D / 2 + 8 * sub + 4);
+  r.a0 = *reinterpret_cast<const float4*>(p + 4 * sub);
+  r.a1 = *reinterpret_cast<const float4*>(p + D / 4 + 4 * sub);
+  r.b0 = *reinterpret_cast<const float4*>(p + D / 2 + 4 * sub);
+  r.b1 = *reinterpret_cast<const float4*>(p + 3 * D / 4 + 4 * sub);
 }
 
 __device__ __forceinline__ float2 bf2(uint32_t w) {
@@ -101,35 +110,38 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* p, int sub, const float
 }
 template <int D>
 __device__ __forceinline__ void store_row(float* p, int sub, const float2 (&x)[8]) {
-  float4* a = reinterpret_cast<float4*>(p + 8 * sub);
-  float4* b = reinterpret_cast<float4*>(p + D / 2 + 8 * sub);
-  a[0] = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
-  a[1] = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
-  b[0] = make_float4(x[4].x, x[4].y, x[5].x, x[5].y);
-  b[1] = make_float4(x[6].x, x[6].y, x[7].x, x[7].y);
+  *reinterpret_cast<float4*>(p + 4 * sub) = make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
+  *reinterpret_cast<float4*>(p + D / 4 + 4 * sub) = make_float4(x[2].x, x[2].y, x[3].x, x[3].y);
+  *reinterpret_cast<float4*>(p + D / 2 + 4 * sub) = make_float4(x[4].x, x[4].y, x[5].x, x[5].y);
+  *reinterpret_cast<float4*>(p + 3 * D / 4 + 4 * sub) = make_float4(x[6].x, x[6].y, x[7].x, x[7].y);
 }
 
 // The 8 (c, s) of this lane's pairs, laid out for rotate(): Half: cs[j] belongs to
 // the features x[j] and x[4 + j]; interleaved: to the pair x[2j], x[2j + 1] split
 // as c[j].x for x[2j], c[j].y for x[2j + 1].
-template <int D, bool kInter>
+template <typename T, int D, bool kInter>
 __device__ __forceinline__ void load_angles(const float* __restrict__ cos_t, const float* __restrict__ sin_t, int pos,
                                             int sub, float2 (&c)[4], float2 (&s)[4]) {
   const size_t row = static_cast<size_t>(pos) * (D / 2);
-  const int o0 = kInter ? 4 * sub : 8 * sub;
-  const int o1 = kInter ? D / 4 + 4 * sub : 8 * sub + 4;
-  const float4 c0 = __ldg(reinterpret_cast<const float4*>(cos_t + row + o0));
-  const float4 c1 = __ldg(reinterpret_cast<const float4*>(cos_t + row + o1));
-  const float4 s0 = __ldg(reinterpret_cast<const float4*>(sin_t + row + o0));
-  const float4 s1 = __ldg(reinterpret_cast<const float4*>(sin_t + row + o1));
-  c[0] = make_float2(c0.x, c0.y);
-  c[1] = make_float2(c0.z, c0.w);
-  c[2] = make_float2(c1.x, c1.y);
-  c[3] = make_float2(c1.z, c1.w);
-  s[0] = make_float2(s0.x, s0.y);
-  s[1] = make_float2(s0.z, s0.w);
-  s[2] = make_float2(s1.x, s1.y);
-  s[3] = make_float2(s1.z, s1.w);
+  if constexpr (kInter && sizeof(T) == 4) {  // a run holds two pairs: two neighbouring angles
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int at = feature<T, D>(2 * k, sub) / 2;
+      c[k] = __ldg(reinterpret_cast<const float2*>(cos_t + row + at));
+      s[k] = __ldg(reinterpret_cast<const float2*>(sin_t + row + at));
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {  // four neighbouring angles each
+      const int at = kInter ? feature<T, D>(2 * k, sub) / 2 : feature<T, D>(k, sub);
+      const float4 vc = __ldg(reinterpret_cast<const float4*>(cos_t + row + at));
+      const float4 vs = __ldg(reinterpret_cast<const float4*>(sin_t + row + at));
+      c[k] = make_float2(vc.x, vc.y);
+      c[k + 1] = make_float2(vc.z, vc.w);
+      s[k] = make_float2(vs.x, vs.y);
+      s[k + 1] = make_float2(vs.z, vs.w);
+    }
+  }
 }
 
 // The rotation (kBack: its transpose) with a gain folded into the angles:
@@ -194,17 +206,27 @@ __device__ __forceinline__ void rotate_back(const float2 (&g)[8], const float2 (
   }
 }
 
-// this lane's 16 gains in the order of x
-template <int D>
+// this lane's 16 gains in the order of x (rows of T, gains of either type)
+template <typename T, int D>
 __device__ __forceinline__ void load_gain(const void* w, int w_f32, int sub, float2 (&o)[8]) {
   if (w_f32) {
-    Raw<float> r;
-    load_row<D>(r, static_cast<const float*>(w), sub);
-    unpack(r, o);
-  } else {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {  // four features each
+      const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + feature<T, D>(2 * r, sub));
+      o[2 * r] = make_float2(v.x, v.y);
+      o[2 * r + 1] = make_float2(v.z, v.w);
+    }
+  } else if constexpr (sizeof(T) == 2) {
     Raw<__nv_bfloat16> r;
     load_row<D>(r, static_cast<const __nv_bfloat16*>(w), sub);
     unpack(r, o);
+  } else {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(w) + feature<T, D>(2 * r, sub));
+      o[2 * r] = bf2(v.x);
+      o[2 * r + 1] = bf2(v.y);
+    }
   }
 }
 
@@ -259,8 +281,8 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 && !kInter ? 5 : 4
   T* o0 = static_cast<T*>(t.out) + static_cast<size_t>(token) * nh * D;
   const int pos = checked_position(a, a.positions ? a.positions[token] : n, lane);
   float2 c[4], s[4], w[8];
-  if (pos >= 0) load_angles<D, kInter>(a.cos_t, a.sin_t, pos, sub, c, s);
-  if (kNorm) load_gain<D>(t.w, a.w_f32, sub, w);
+  if (pos >= 0) load_angles<T, D, kInter>(a.cos_t, a.sin_t, pos, sub, c, s);
+  if (kNorm) load_gain<T, D>(t.w, a.w_f32, sub, w);
   Coef k;
   if (pos >= 0) make_coef<kInter, kNorm>(c, s, w, k);
   for (int it = 0; it < a.per && (group * a.per + it) * kRows < nh; it += kAhead) {
@@ -317,6 +339,9 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void copy16_l1(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void copy8_l1(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
 template <int kPending>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
@@ -338,16 +363,14 @@ __device__ __forceinline__ void lds_row(uint32_t addr, Raw<float>& r) {
   r.b0 = lds_f4(addr + 2 * kStep);
   r.b1 = lds_f4(addr + 3 * kStep);
 }
-// this lane's 16 features of the row at p into its slots from dst on
+// this lane's 16 features of the row at p into its slots from dst on, run by run
 template <int D, typename T>
 __device__ __forceinline__ void copy_row(uint32_t dst, const T* p, int sub) {
   constexpr int kStep = kWarps * 32 * 16;
-  constexpr int kHalf = 8 * sizeof(T) / 16;
+  constexpr int kRun = 16 / sizeof(T);
+  constexpr int kRuns = 16 / kRun;
 #pragma unroll
-  for (int i = 0; i < kHalf; ++i) {
-    copy16(dst + i * kStep, p + 8 * sub + i * (16 / sizeof(T)));
-    copy16(dst + (kHalf + i) * kStep, p + D / 2 + 8 * sub + i * (16 / sizeof(T)));
-  }
+  for (int i = 0; i < kRuns; ++i) copy16(dst + i * kStep, p + i * (D / kRuns) + kRun * sub);
 }
 
 // A warp's walk over its units (a position, a group of rows) and their iterations.
@@ -404,7 +427,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_bwd_kernel(const RopeArgs
   const uint32_t rows_at = smem_u32(ring) + threadIdx.x * 16;
   const uint32_t angles_at = rows_at + R::kStages * R::kPieces * kStep;
   float2 w[8], acc[8];
-  if (kNorm) load_gain<D>(t.w, a.w_f32, sub, w);
+  if (kNorm) load_gain<T, D>(t.w, a.w_f32, sub, w);
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] = make_float2(0.f, 0.f);
 
@@ -422,12 +445,22 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_bwd_kernel(const RopeArgs
         xp = static_cast<const T*>(t.x) + b * t.sb + n * t.sn;
         if (ahead.pos >= 0) {
           const size_t row = static_cast<size_t>(ahead.pos) * (D / 2);
-          const int o0 = kInter ? 4 * sub : 8 * sub, o1 = kInter ? D / 4 + 4 * sub : 8 * sub + 4;
           const uint32_t dst = angles_at + ahead_unit * 4 * kStep;
-          copy16_l1(dst, a.cos_t + row + o0);
-          copy16_l1(dst + kStep, a.cos_t + row + o1);
-          copy16_l1(dst + 2 * kStep, a.sin_t + row + o0);
-          copy16_l1(dst + 3 * kStep, a.sin_t + row + o1);
+          if constexpr (kInter && sizeof(T) == 4) {  // as load_angles
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int at = feature<T, D>(2 * k, sub) / 2;
+              copy8_l1(dst + (k >> 1) * kStep + (k & 1) * 8, a.cos_t + row + at);
+              copy8_l1(dst + (2 + (k >> 1)) * kStep + (k & 1) * 8, a.sin_t + row + at);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+              const int at = kInter ? feature<T, D>(2 * k, sub) / 2 : feature<T, D>(k, sub);
+              copy16_l1(dst + (k >> 1) * kStep, a.cos_t + row + at);
+              copy16_l1(dst + (2 + (k >> 1)) * kStep, a.sin_t + row + at);
+            }
+          }
         }
         ahead_unit = ahead_unit + 1 == R::kStages ? 0 : ahead_unit + 1;
       }
@@ -514,7 +547,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_bwd_kernel(const RopeArgs
         v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
       }
       if (lane < kLanes) {
-        const int f = (j < 4 ? 0 : D / 2) + 8 * sub + 2 * (j & 3);
+        const int f = feature<T, D>(j, sub);
         sums[warp][f] = v.x;
         sums[warp][f + 1] = v.y;
       }

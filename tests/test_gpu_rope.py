@@ -65,6 +65,8 @@ CASES = [
     (F32, 3, 21, 6, 3, 128, False, False, False, True, F32),
     (BF, 2, 19, 0, 3, 64, True, False, False, True, BF),       # keys alone
     (F32, 2, 19, 3, 3, 64, True, False, False, True, BF),      # gains in fewer bits than the rows
+    (F32, 2, 23, 5, 1, 128, True, True, True, True, BF),
+    (F32, 1, 41, 9, 3, 128, False, True, False, False, F32),
 ]
 
 
