@@ -904,16 +904,21 @@ RopeArgs rope_args(const void* Q, const void* K, const void* wq, const void* wk,
 
 // Blocks of the backward: as many as fill the GPU, shared between q and k by their work.
 void rope_blocks(RopeArgs* a, int d) {
+  const int rows = 512 / d;
+  a->q_groups = (a->H + rows - 1) / rows;
+  a->k_groups = (a->Hkv + rows - 1) / rows;
+  a->per = 8;  // of a warp and round
+  // two row groups or more a warp
   const long long qu = static_cast<long long>(a->tokens) * a->q_groups, ku = static_cast<long long>(a->tokens) * a->k_groups;
-  const long long qw = (qu + kRopeBlockWarps - 1) / kRopeBlockWarps, kw = (ku + kRopeBlockWarps - 1) / kRopeBlockWarps;
+  const int least = 2 * kRopeBlockWarps;
+  const long long qw = (qu + least - 1) / least, kw = (ku + least - 1) / least;
   if (qw + kw <= kRopeBwdBlocks) {
     a->q_blocks = static_cast<int>(qw);
     a->blocks = static_cast<int>(qw + kw);
     return;
   }
-  // by their row groups, and one more for each unit's start
-  const int rows = 512 / d;
-  const long long qc = (a->H + rows - 1) / rows + a->q_groups, kc = (a->Hkv + rows - 1) / rows + a->k_groups;
+  // by their row groups, and one more for each position's start
+  const long long qc = a->q_groups + (a->H > 0), kc = a->k_groups + (a->Hkv > 0);
   const long long want = std::max<long long>(a->H ? 1 : 0, kRopeBwdBlocks * qc / (qc + kc));
   a->q_blocks = static_cast<int>(std::min(qw, std::min<long long>(want, kRopeBwdBlocks - (a->Hkv ? 1 : 0))));
   a->blocks = a->q_blocks + static_cast<int>(std::min(kw, static_cast<long long>(kRopeBwdBlocks - a->q_blocks)));

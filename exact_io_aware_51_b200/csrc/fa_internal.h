@@ -178,8 +178,10 @@ struct RopeArgs {
   const int* positions;  // [B, N] or nullptr: 0 .. N - 1
   int tokens, N;         // tokens = B * N
   int H, Hkv, table;
-  int per;               // row groups (of 512 / d heads) a warp takes at one position
-  int q_groups, k_groups;  // warps per position for q and k
+  // row groups (of 512 / d heads): how many a warp takes at one position (forward) or in
+  // one round (backward); warps (forward) or row groups (backward) of a position in q and k
+  int per;
+  int q_groups, k_groups;
   int interleaved, w_f32;
   float eps;
   int* status;

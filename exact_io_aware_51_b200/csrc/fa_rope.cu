@@ -24,7 +24,7 @@
 //
 // Measured on a B200 (GPU time), d = 128, bf16: forward B1 N16384 H32 + 32 (537 MB) 85
 // us, 6.3 TB/s; B1 N4096 H64 + 8 out of a packed projection (151 MB) 28 us, 5.4 TB/s;
-// backward B1 N16384 H32 + 32 (805 MB) 144 us with the gains' sums, 5.6 TB/s.
+// backward B1 N16384 H32 + 32 (805 MB) 131 us with the gains' sums, 6.1 TB/s.
 // fp32: B2 N4096 H32 + 8 forward (335 MB) 61 us, 5.5 TB/s; backward (503 MB) 86 us, 5.9
 // TB/s (130 us with a lane's 8 features of a half side by side: 32-byte steps).
 #include <cuda_bf16.h>
@@ -317,8 +317,8 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 && !kInter ? 5 : 4
 }
 
 // ---------------------------------------------------------------------------
-// Backward: blocks [0, q_blocks) walk the (position, head group) units of q, the
-// others those of k, each warp with its own running sum of the gain's gradient;
+// Backward: blocks [0, q_blocks) walk the row groups (512 / d heads at one position) of
+// q, the others those of k, each warp with its own running sum of the gain's gradient;
 // a block writes the sum of its warps to partial[block][d].
 // ---------------------------------------------------------------------------
 template <typename T, int D, bool kNorm>
@@ -326,8 +326,9 @@ struct BwdRing {
   // Rows and angles of the next iterations wait in shared memory, written by asynchronous
   // copies into slots of the lane's own (no barrier): the registers that the
   // gradient needs leave room for 12 warps on an SM, whose own loads would keep only
-  // 24 KB in flight.
-  static constexpr int kStages = sizeof(T) == 2 ? 4 : 3;
+  // 24 KB in flight.  Three stages: B1 N16384 H32 + 32 d128 bf16 takes 131 us (2: 135; 4:
+  // 143, more streams than memory likes); four were 1% better on smaller ones at best.
+  static constexpr int kStages = 3;
   static constexpr int kRow = 16 * sizeof(T) / 16;             // 16-byte pieces of a lane's 16 features
   static constexpr int kPieces = (kNorm ? 2 : 1) * kRow;       // g, then x
   static constexpr int kBytes = kStages * (kPieces + 4) * kWarps * 32 * 16;
@@ -373,32 +374,76 @@ __device__ __forceinline__ void copy_row(uint32_t dst, const T* p, int sub) {
   for (int i = 0; i < kRuns; ++i) copy16(dst + i * kStep, p + i * (D / kRuns) + kRun * sub);
 }
 
-// A warp's walk over its units (a position, a group of rows) and their iterations.
-struct Units {
-  unsigned int u, units, stride;  // unit, their number, step (units + stride < 2^32, host check)
-  int groups, nh, rows;
-  int it, its;        // iteration, iterations of the unit
-  int h0;             // head of this lane's row at iteration 0
-  int token, pos;
-  int coming;         // position of the next unit's token, asked for a unit ahead
-  __device__ __forceinline__ bool more() const { return u < units; }
-  __device__ __forceinline__ int raw_position(const RopeArgs& a, unsigned int unit) const {
-    if (unit >= units) return -1;
-    const int tok = static_cast<int>(unit / static_cast<unsigned int>(groups));
+// A warp's walk over row groups, counted through all positions (fewer than 2^32: B N H d
+// < 2^40).  In rounds, every warp takes the next `per` groups, so that the GPU reads one
+// stretch of memory at a time; what is left for no full round is cut into equal ranges.
+// Without the cut, whole ranges of a position: B1 N8192 H40 + 40 d128 101 us for 81.  One
+// range per warp, and no rounds: H32 + 32 N16384 139 us for 131, d64 133 for 125.
+struct Shares {
+  unsigned int groups;          // of a position
+  unsigned int per, step;       // of a warp's range, of a round
+  unsigned int last, last_end;  // this warp's range of the rest
+};
+struct Walk {
+  unsigned int g, end;    // the position's first group in this range, end of the range
+  unsigned int ng, nend;  // the range after it (empty: none)
+  int rounds;             // full rounds after that one; -1: the rest is given out, too
+  int it, its;            // iteration, iterations at this position
+  int group;              // first group at this position
+  int token, ntoken;      // position in [0, B N): this one, the next range's first
+  int pos, coming;        // the caller's: this one's, the next one's (asked for one ahead)
+  __device__ __forceinline__ bool more() const { return g < end; }
+  static __device__ __forceinline__ int raw_position(const RopeArgs& a, int tok) {
     return a.positions ? a.positions[tok] : tok % a.N;
   }
-  __device__ __forceinline__ void open(const RopeArgs& a, int raw, int lane_row, int lane) {  // unit u < units
-    token = static_cast<int>(u / static_cast<unsigned int>(groups));
-    const int first = static_cast<int>(u - static_cast<unsigned int>(token) * groups) * a.per * rows;
+  __device__ __forceinline__ void open(const RopeArgs& a, const Shares& w, int raw, int lane) {  // g < end
     pos = checked_position(a, raw, lane);
-    coming = raw_position(a, u + stride);
-    its = min(a.per, (nh - first + rows - 1) / rows);
-    h0 = first + lane_row;
+    its = static_cast<int>(min(end - g, w.groups - group));
     it = 0;
+    if (end - g > static_cast<unsigned int>(its)) {
+      coming = raw_position(a, token + 1);
+    } else if (ng < nend) {
+      ntoken = static_cast<int>(ng / w.groups);
+      coming = raw_position(a, ntoken);
+    }
   }
-  __device__ __forceinline__ void next(const RopeArgs& a, int lane_row, int lane) {
-    u += stride;
-    if (more()) open(a, coming, lane_row, lane);
+  // the range after [ng, nend)
+  __device__ __forceinline__ void after(const Shares& w) {
+    if (rounds > 0) {
+      ng += w.step;
+      nend = ng + w.per;
+    } else {
+      ng = rounds == 0 ? w.last : nend;
+      nend = rounds == 0 ? w.last_end : nend;
+    }
+    rounds = max(rounds - 1, -1);
+  }
+  __device__ __forceinline__ void first(const RopeArgs& a, const Shares& w, unsigned int mine, int full, int lane) {
+    g = full ? mine * w.per : w.last;
+    end = full ? g + w.per : w.last_end;
+    rounds = full - 1;
+    ng = g;
+    nend = end;
+    after(w);
+    if (!more()) return;
+    token = static_cast<int>(g / w.groups);
+    group = static_cast<int>(g - static_cast<unsigned int>(token) * w.groups);
+    open(a, w, raw_position(a, token), lane);
+  }
+  __device__ __forceinline__ void next(const RopeArgs& a, const Shares& w, int lane) {
+    g += its;
+    if (more()) {
+      ++token;
+      group = 0;
+    } else {
+      g = ng;
+      end = nend;
+      if (!more()) return;
+      after(w);
+      token = ntoken;
+      group = static_cast<int>(g - static_cast<unsigned int>(token) * w.groups);
+    }
+    open(a, w, coming, lane);
   }
 };
 
@@ -417,13 +462,15 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_bwd_kernel(const RopeArgs
   const int blocks = is_q ? a.q_blocks : static_cast<int>(gridDim.x) - a.q_blocks;
   const int nh = is_q ? a.H : a.Hkv;
   const RopeTensor& t = is_q ? a.q : a.k;
-  Units at;
-  at.groups = is_q ? a.q_groups : a.k_groups;
-  at.nh = nh;
-  at.rows = kRows;
-  at.units = static_cast<unsigned int>(a.tokens) * static_cast<unsigned int>(at.groups);
-  at.stride = static_cast<unsigned int>(blocks) * kWarps;
-  at.u = static_cast<unsigned int>(first) * kWarps + warp;
+  Shares share;
+  share.groups = is_q ? a.q_groups : a.k_groups;
+  share.per = a.per;
+  const unsigned int total = static_cast<unsigned int>(a.tokens) * share.groups;
+  const unsigned int warps = blocks * kWarps, mine = first * kWarps + warp;
+  share.step = warps * share.per;
+  const unsigned int full = total / share.step, rest = total - full * share.step;  // rest * warps < 2^32
+  share.last = full * share.step + rest * mine / warps;
+  share.last_end = full * share.step + rest * (mine + 1) / warps;
   const uint32_t rows_at = smem_u32(ring) + threadIdx.x * 16;
   const uint32_t angles_at = rows_at + R::kStages * R::kPieces * kStep;
   float2 w[8], acc[8];
@@ -432,8 +479,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_bwd_kernel(const RopeArgs
   for (int j = 0; j < 8; ++j) acc[j] = make_float2(0.f, 0.f);
 
   // the copies of one iteration, as one group (which may be empty)
-  if (at.more()) at.open(a, at.raw_position(a, at.u), lane / kLanes, lane);
-  Units ahead = at;
+  Walk at;
+  at.first(a, share, mine, static_cast<int>(full), lane);
+  Walk ahead = at;
   int ahead_row = 0, ahead_unit = 0;  // slots
   const T* gp = nullptr;
   const T* xp = nullptr;
@@ -464,13 +512,13 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_bwd_kernel(const RopeArgs
         }
         ahead_unit = ahead_unit + 1 == R::kStages ? 0 : ahead_unit + 1;
       }
-      const int h = ahead.h0 + ahead.it * kRows;
+      const int h = (ahead.group + ahead.it) * kRows + lane / kLanes;
       if (ahead.pos >= 0 && h < nh) {
         const uint32_t dst = rows_at + ahead_row * R::kPieces * kStep;
         copy_row<D>(dst, gp + h * t.gh, sub);
         if (kNorm) copy_row<D>(dst + R::kRow * kStep, xp + h * t.sh, sub);
       }
-      if (++ahead.it == ahead.its) ahead.next(a, lane / kLanes, lane);
+      if (++ahead.it == ahead.its) ahead.next(a, share, lane);
     }
     ahead_row = ahead_row + 1 == R::kStages ? 0 : ahead_row + 1;
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -496,7 +544,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_bwd_kernel(const RopeArgs
       }
       const uint32_t src = rows_at + row_slot * R::kPieces * kStep;
       row_slot = row_slot + 1 == R::kStages ? 0 : row_slot + 1;
-      const int h = at.h0 + at.it * kRows;
+      const int h = (at.group + at.it) * kRows + lane / kLanes;
       const bool ok = h < nh;
       float2 o[8];
 #pragma unroll
@@ -532,7 +580,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_bwd_kernel(const RopeArgs
       }
       if (ok) store_row<D>(o0 + static_cast<size_t>(h) * D, sub, o);
     }
-    at.next(a, lane / kLanes, lane);
+    at.next(a, share, lane);
   }
   copies_wait<0>();
 
