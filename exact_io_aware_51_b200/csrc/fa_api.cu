@@ -828,11 +828,10 @@ int fa_decode_paged(const void* Q, const void* K_cache, const void* V_cache, con
 // ---------------------------------------------------------------------------
 namespace {
 
-// Row groups per warp: as many as the tensor with more heads has, at most 8, but fewer
-// where that leaves less than about two rounds of warps (148 SMs x 64).
-constexpr long long kFullWarps = 148LL * 64;
 constexpr int kRopeBlockWarps = 4;
-constexpr int kRopeBwdBlocks = 148 * 3;  // resident together
+constexpr int kRopeFwdBlocks = 148 * 4;  // resident together
+constexpr int kRopeBwdBlocks = 148 * 3;
+constexpr int kRopeRound = 8;            // row groups (of 512 / d heads) of a warp in one round
 
 bool aligned_strides(const long long* s, int dtype) {
   const long long m = dtype == FA_BF16 ? 8 : 4;  // 16 bytes
@@ -893,35 +892,29 @@ RopeArgs rope_args(const void* Q, const void* K, const void* wq, const void* wk,
   a.eps = eps;
   a.status = status;
   const int rows = 512 / d;
-  const int qg = (H + rows - 1) / rows, kg = (Hkv + rows - 1) / rows;
-  auto warps = [&](int per) { return static_cast<long long>(a.tokens) * ((qg + per - 1) / per + (kg + per - 1) / per); };
-  a.per = 8;
-  while (a.per > 2 && (a.per / 2 >= std::max(qg, kg) || warps(a.per) < kFullWarps)) a.per /= 2;
-  a.q_groups = (H + rows * a.per - 1) / (rows * a.per);
-  a.k_groups = (Hkv + rows * a.per - 1) / (rows * a.per);
+  a.q_groups = (H + rows - 1) / rows;
+  a.k_groups = (Hkv + rows - 1) / rows;
   return a;
 }
 
-// Blocks of the backward: as many as fill the GPU, shared between q and k by their work.
-void rope_blocks(RopeArgs* a, int d) {
-  const int rows = 512 / d;
-  a->q_groups = (a->H + rows - 1) / rows;
-  a->k_groups = (a->Hkv + rows - 1) / rows;
-  a->per = 8;  // of a warp and round
+// Blocks that walk the row groups in rounds: as many as fill the GPU, shared between q
+// and k by their work.
+void rope_rounds(RopeArgs* a, int per, long long most) {
+  a->per = per;
   // two row groups or more a warp
   const long long qu = static_cast<long long>(a->tokens) * a->q_groups, ku = static_cast<long long>(a->tokens) * a->k_groups;
   const int least = 2 * kRopeBlockWarps;
   const long long qw = (qu + least - 1) / least, kw = (ku + least - 1) / least;
-  if (qw + kw <= kRopeBwdBlocks) {
+  if (qw + kw <= most) {
     a->q_blocks = static_cast<int>(qw);
     a->blocks = static_cast<int>(qw + kw);
     return;
   }
   // by their row groups, and one more for each position's start
   const long long qc = a->q_groups + (a->H > 0), kc = a->k_groups + (a->Hkv > 0);
-  const long long want = std::max<long long>(a->H ? 1 : 0, kRopeBwdBlocks * qc / (qc + kc));
-  a->q_blocks = static_cast<int>(std::min(qw, std::min<long long>(want, kRopeBwdBlocks - (a->Hkv ? 1 : 0))));
-  a->blocks = a->q_blocks + static_cast<int>(std::min(kw, static_cast<long long>(kRopeBwdBlocks - a->q_blocks)));
+  const long long want = std::max<long long>(a->H ? 1 : 0, most * qc / (qc + kc));
+  a->q_blocks = static_cast<int>(std::min(qw, std::min<long long>(want, most - (a->Hkv ? 1 : 0))));
+  a->blocks = a->q_blocks + static_cast<int>(std::min(kw, most - a->q_blocks));
 }
 
 }  // namespace
@@ -939,8 +932,20 @@ int fa_qk_norm_rope(const void* Q, const void* K, const void* q_weight, const vo
   if (!aligned_strides(q_strides, dtype) || !aligned_strides(k_strides, dtype)) return FA_ERR_MISALIGNED;
   DeviceState* st = nullptr;
   if ((rc = device_state(&st))) return rc;
-  const RopeArgs a = rope_args(Q, K, q_weight, k_weight, cos_table, sin_table, positions, Q_out, K_out, B, N, H, Hkv, d,
+  RopeArgs a = rope_args(Q, K, q_weight, k_weight, cos_table, sin_table, positions, Q_out, K_out, B, N, H, Hkv, d,
                                q_strides, k_strides, table_rows, eps, interleaved, weight_dtype, st->status);
+  const long long groups = static_cast<long long>(a.tokens) * (a.q_groups + a.k_groups);
+  if (groups >= kRopeFwdBlocks * kRopeBlockWarps * kRopeRound) {
+    // From one full round on, bf16 d128: B1 N2048 H32 + 8 (20480 groups) 8.5 us against 9.3 by
+    // pairs; d64 B4 N1001 H16 + 4 (12012 groups) 6.6 against 5.7.  Rounds of half the size from
+    // 400 MB on: B1 N15000 H32 + 32 (492 MB) 80 us against 88, B4 N8192 H32 + 8 (671 MB) 111
+    // against 116; B2 N8192 H32 + 8 (336 MB) 57.5 against 56.2, B1 N4096 H64 + 8 27.5 against 26.
+    const double bytes = 2.0 * a.tokens * (H + Hkv) * d * (dtype == FA_FP32 ? 4 : 2);
+    rope_rounds(&a, bytes < 400e6 ? kRopeRound : kRopeRound / 2, kRopeFwdBlocks);
+  } else {  // pairs of groups, a warp each
+    a.q_groups = (a.q_groups + 1) / 2;
+    a.k_groups = (a.k_groups + 1) / 2;
+  }
   const cudaError_t e = launch_rope_fwd(a, d, dtype == FA_FP32, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : fail_cuda(e);
 }
@@ -980,7 +985,7 @@ int fa_qk_norm_rope_bwd(const void* Q, const void* K, const void* q_weight, cons
   a.k.g = dK_out;
   set_strides(dq_out_strides, N, H, d, &a.q.gb, &a.q.gn, &a.q.gh);
   set_strides(dk_out_strides, N, Hkv, d, &a.k.gb, &a.k.gn, &a.k.gh);
-  if (!empty) rope_blocks(&a, d);
+  if (!empty) rope_rounds(&a, kRopeRound, kRopeBwdBlocks);
   a.partial = static_cast<float*>(workspace);
   a.dwq = dq_weight;
   a.dwk = dk_weight;

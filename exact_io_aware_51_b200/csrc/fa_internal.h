@@ -178,15 +178,13 @@ struct RopeArgs {
   const int* positions;  // [B, N] or nullptr: 0 .. N - 1
   int tokens, N;         // tokens = B * N
   int H, Hkv, table;
-  // row groups (of 512 / d heads): how many a warp takes at one position (forward) or in
-  // one round (backward); warps (forward) or row groups (backward) of a position in q and k
-  int per;
-  int q_groups, k_groups;
+  int q_groups, k_groups;  // row groups (of 512 / d heads) of a position; forward without rounds: pairs of them
+  int per;                 // row groups of a warp in one round
   int interleaved, w_f32;
   float eps;
   int* status;
+  int q_blocks, blocks;  // blocks of q, and of both (0: forward without rounds)
   // backward
-  int q_blocks, blocks;  // blocks of q, and of both
   float* partial;        // [blocks, d] fp32 sums of the gains' gradients
   void* dwq;
   void* dwk;

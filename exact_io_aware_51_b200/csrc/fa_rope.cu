@@ -22,10 +22,10 @@
 // and gains are read once for all of them.  All arithmetic is fp32 (packed
 // pairs), each output is rounded once.
 //
-// Measured on a B200 (GPU time), d = 128, bf16: forward B1 N16384 H32 + 32 (537 MB) 85
-// us, 6.3 TB/s; B1 N4096 H64 + 8 out of a packed projection (151 MB) 28 us, 5.4 TB/s;
+// Measured on a B200 (GPU time), d = 128, bf16: forward B1 N16384 H32 + 32 (537 MB) 86
+// us, 6.3 TB/s; B1 N4096 H64 + 8 out of a packed projection (151 MB) 26 us, 5.8 TB/s;
 // backward B1 N16384 H32 + 32 (805 MB) 131 us with the gains' sums, 6.1 TB/s.
-// fp32: B2 N4096 H32 + 8 forward (335 MB) 61 us, 5.5 TB/s; backward (503 MB) 86 us, 5.9
+// fp32: B2 N4096 H32 + 8 forward (335 MB) 59 us, 5.7 TB/s; backward (503 MB) 86 us, 5.9
 // TB/s (130 us with a lane's 8 features of a half side by side: 32-byte steps).
 #include <cuda_bf16.h>
 
@@ -255,14 +255,31 @@ __device__ __forceinline__ int checked_position(const RopeArgs& a, int pos, int 
   return pos;
 }
 
+// one row of the forward: every lane of the warp comes here, its row valid or not
+template <int D, bool kNorm, bool kInter, typename T>
+__device__ __forceinline__ void turn_row(const Raw<T>& raw, int pos, const Coef& k, float eps, float2 (&o)[8]) {
+  if (pos >= 0) {
+    float2 x[8];
+    unpack(raw, x);
+    float r = 1.f;
+    if constexpr (kNorm) r = row_rsqrt<D>(x, eps);
+    rotate<kInter>(x, k, o);
+    if constexpr (kNorm) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = fmul2(o[j], make_float2(r, r));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = make_float2(0.f, 0.f);
+  }
+}
+
 // ---------------------------------------------------------------------------
-// Forward: a warp takes `per` groups of rows (4 heads of d = 128, 8 of d = 64)
-// of one tensor at one position; grid (position blocks, head groups of q then k).
+// Forward, few rows: a warp takes two groups of rows (4 heads of d = 128, 8 of d = 64) of
+// one tensor at one position, both loaded before the first is used; grid (position
+// blocks, pairs of groups of q then k).
 // ---------------------------------------------------------------------------
-// kAhead rows are loaded before the first is used.  Measured at B1 N16384 H32 + 32 d128
-// bf16 (537 MB): 4 rows at 5 blocks per SM 85 us, 2 rows 95 us; 4 blocks or spilled
-// registers at 6 87..91 us.  A warp with two row groups has no use for four.
-template <typename T, int D, bool kNorm, bool kInter, int kAhead>
+template <typename T, int D, bool kNorm, bool kInter>
 __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 && !kInter ? 5 : 4) rope_fwd_kernel(const RopeArgs a) {
   constexpr int kLanes = D / 16;
   constexpr int kRows = 32 / kLanes;
@@ -272,66 +289,53 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 && !kInter ? 5 : 4
   if (token >= a.tokens) return;
   const int sub = lane % kLanes;
   const bool is_q = static_cast<int>(blockIdx.y) < a.q_groups;
-  const int group = is_q ? blockIdx.y : blockIdx.y - a.q_groups;
+  const int pair = is_q ? blockIdx.y : blockIdx.y - a.q_groups;
   const int nh = is_q ? a.H : a.Hkv;
-  const int h0 = group * a.per * kRows + lane / kLanes;
+  const int h0 = pair * 2 * kRows + lane / kLanes;
   const int b = token / a.N, n = token - b * a.N;
   const RopeTensor& t = is_q ? a.q : a.k;
   const T* x0 = static_cast<const T*>(t.x) + b * t.sb + n * t.sn;
   T* o0 = static_cast<T*>(t.out) + static_cast<size_t>(token) * nh * D;
   const int pos = checked_position(a, a.positions ? a.positions[token] : n, lane);
+  constexpr int kAhead = sizeof(T) == 2 ? 2 : 1;  // registers
+  Raw<T> raw[2];
+  auto load = [&](int u) {
+    raw[u] = {};
+    if (pos >= 0 && h0 + u * kRows < nh) load_row<D>(raw[u], x0 + (h0 + u * kRows) * t.sh, sub);
+  };
   float2 c[4], s[4], w[8];
   if (pos >= 0) load_angles<T, D, kInter>(a.cos_t, a.sin_t, pos, sub, c, s);
   if (kNorm) load_gain<T, D>(t.w, a.w_f32, sub, w);
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) load(u);
   Coef k;
   if (pos >= 0) make_coef<kInter, kNorm>(c, s, w, k);
-  for (int it = 0; it < a.per && (group * a.per + it) * kRows < nh; it += kAhead) {
-    Raw<T> raw[kAhead];
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int h = h0 + (it + u) * kRows;
-      raw[u] = {};
-      if (pos >= 0 && it + u < a.per && h < nh) load_row<D>(raw[u], x0 + h * t.sh, sub);
-    }
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const int h = h0 + (it + u) * kRows;
-      float2 o[8];
-      if (pos >= 0) {
-        float2 x[8];
-        unpack(raw[u], x);
-        float r = 1.f;
-        if constexpr (kNorm) r = row_rsqrt<D>(x, a.eps);  // every lane of the warp, its row valid or not
-        rotate<kInter>(x, k, o);
-        if constexpr (kNorm) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = fmul2(o[j], make_float2(r, r));
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = make_float2(0.f, 0.f);
-      }
-      if (it + u < a.per && h < nh) store_row<D>(o0 + static_cast<size_t>(h) * D, sub, o);
-    }
+  for (int u = 0; u < 2; ++u) {
+    if (u && pair * 2 * kRows + kRows >= nh) break;  // no row of the second group
+    if (u >= kAhead) load(u);
+    float2 o[8];
+    turn_row<D, kNorm, kInter>(raw[u], pos, k, a.eps, o);
+    if (h0 + u * kRows < nh) store_row<D>(o0 + static_cast<size_t>(h0 + u * kRows) * D, sub, o);
   }
 }
 
 // ---------------------------------------------------------------------------
-// Backward: blocks [0, q_blocks) walk the row groups (512 / d heads at one position) of
-// q, the others those of k, each warp with its own running sum of the gain's gradient;
-// a block writes the sum of its warps to partial[block][d].
+// Forward of many rows, and backward: blocks [0, q_blocks) walk the row groups (512 / d
+// heads at one position) of q, the others those of k.  Rows and angles of the next
+// iterations wait in shared memory, written by asynchronous copies into slots of the
+// lane's own (no barrier).
 // ---------------------------------------------------------------------------
-template <typename T, int D, bool kNorm>
-struct BwdRing {
-  // Rows and angles of the next iterations wait in shared memory, written by asynchronous
-  // copies into slots of the lane's own (no barrier): the registers that the
-  // gradient needs leave room for 12 warps on an SM, whose own loads would keep only
-  // 24 KB in flight.  Three stages: B1 N16384 H32 + 32 d128 bf16 takes 131 us (2: 135; 4:
-  // 143, more streams than memory likes); four were 1% better on smaller ones at best.
+// kTensors rows per iteration (x; or g and x).  Three stages, measured at B1 N16384 H32 +
+// 32 d128 bf16: backward 131 us (2: 135; 4: 143, more streams than memory likes; 1% better
+// on smaller ones at best); forward 86 (2: 94, 4: 86), B2 N8192 H32 + 8 56 (2: 60, 4: 62).
+template <typename T, int kTensors>
+struct Ring {
   static constexpr int kStages = 3;
+  static constexpr int kStep = kWarps * 32 * 16;               // a piece of every lane
   static constexpr int kRow = 16 * sizeof(T) / 16;             // 16-byte pieces of a lane's 16 features
-  static constexpr int kPieces = (kNorm ? 2 : 1) * kRow;       // g, then x
-  static constexpr int kBytes = kStages * (kPieces + 4) * kWarps * 32 * 16;
+  static constexpr int kPieces = kTensors * kRow;
+  static constexpr int kBytes = kStages * (kPieces + 4) * kStep;  // and the angles
 };
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
@@ -447,13 +451,61 @@ struct Walk {
   }
 };
 
+// warp `mine`'s shares of the row groups; returns the full rounds
+__device__ __forceinline__ int give_shares(Shares& s, const RopeArgs& a, int groups, unsigned int mine,
+                                           unsigned int warps) {
+  s.groups = groups;
+  s.per = a.per;
+  s.step = warps * s.per;
+  const unsigned int total = static_cast<unsigned int>(a.tokens) * groups;
+  const unsigned int full = total / s.step, rest = total - full * s.step;  // rest * warps < 2^32
+  s.last = full * s.step + rest * mine / warps;
+  s.last_end = full * s.step + rest * (mine + 1) / warps;
+  return static_cast<int>(full);
+}
+
+// a position's angles into this lane's four slots (as load_angles: cosines, then sines)
+template <typename T, int D, bool kInter>
+__device__ __forceinline__ void copy_angles(uint32_t dst, const float* cos_t, const float* sin_t, int pos, int sub) {
+  constexpr int kStep = kWarps * 32 * 16;
+  const size_t row = static_cast<size_t>(pos) * (D / 2);
+  if constexpr (kInter && sizeof(T) == 4) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int at = feature<T, D>(2 * k, sub) / 2;
+      copy8_l1(dst + (k >> 1) * kStep + (k & 1) * 8, cos_t + row + at);
+      copy8_l1(dst + (2 + (k >> 1)) * kStep + (k & 1) * 8, sin_t + row + at);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+      const int at = kInter ? feature<T, D>(2 * k, sub) / 2 : feature<T, D>(k, sub);
+      copy16_l1(dst + (k >> 1) * kStep, cos_t + row + at);
+      copy16_l1(dst + (2 + (k >> 1)) * kStep, sin_t + row + at);
+    }
+  }
+}
+__device__ __forceinline__ void lds_angles(uint32_t src, float2 (&c)[4], float2 (&s)[4]) {
+  constexpr int kStep = kWarps * 32 * 16;
+  const float4 c0 = lds_f4(src), c1 = lds_f4(src + kStep), s0 = lds_f4(src + 2 * kStep), s1 = lds_f4(src + 3 * kStep);
+  c[0] = make_float2(c0.x, c0.y), c[1] = make_float2(c0.z, c0.w);
+  c[2] = make_float2(c1.x, c1.y), c[3] = make_float2(c1.z, c1.w);
+  s[0] = make_float2(s0.x, s0.y), s[1] = make_float2(s0.z, s0.w);
+  s[2] = make_float2(s1.x, s1.y), s[3] = make_float2(s1.z, s1.w);
+}
+
+// The forward at 4 blocks per SM (120 registers; 5 spill).  Against warps with one position
+// each and four rows loaded ahead, bf16 d128: B1 N4096 H64 + 8 26.0 us (27.3), B2 N8192 H32 +
+// 8 56.2 (60), B1 N8192 H40 + 40 55.8 (60.8), B1 N16384 H32 + 32 85.8 (84.4); fp32: B2
+// N4096 H32 + 8 58.6 (60.7), d64 B4 N2048 H16 + 16 22 (28.4).  The norm stands before the
+// rotation in turn_row: the other order took 10% more at N16384.
 template <typename T, int D, bool kNorm, bool kInter>
-__global__ void __launch_bounds__(kWarps * 32, 3) rope_bwd_kernel(const RopeArgs a) {
-  using R = BwdRing<T, D, kNorm>;
+__global__ void __launch_bounds__(kWarps * 32, 4) rope_fwd_rounds_kernel(const RopeArgs a) {
+  using R = Ring<T, 1>;
   extern __shared__ __align__(16) uint8_t ring[];
   constexpr int kLanes = D / 16;
   constexpr int kRows = 32 / kLanes;
-  constexpr int kStep = kWarps * 32 * 16;
+  constexpr int kStep = R::kStep;
   wait_for_previous_kernel();
   const int lane = lane_id(), warp = warp_id();
   const int sub = lane % kLanes;
@@ -463,14 +515,82 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_bwd_kernel(const RopeArgs
   const int nh = is_q ? a.H : a.Hkv;
   const RopeTensor& t = is_q ? a.q : a.k;
   Shares share;
-  share.groups = is_q ? a.q_groups : a.k_groups;
-  share.per = a.per;
-  const unsigned int total = static_cast<unsigned int>(a.tokens) * share.groups;
   const unsigned int warps = blocks * kWarps, mine = first * kWarps + warp;
-  share.step = warps * share.per;
-  const unsigned int full = total / share.step, rest = total - full * share.step;  // rest * warps < 2^32
-  share.last = full * share.step + rest * mine / warps;
-  share.last_end = full * share.step + rest * (mine + 1) / warps;
+  const int full = give_shares(share, a, is_q ? a.q_groups : a.k_groups, mine, warps);
+  const uint32_t rows_at = smem_u32(ring) + threadIdx.x * 16;
+  const uint32_t angles_at = rows_at + R::kStages * R::kRow * kStep;
+  float2 w[8];
+  if (kNorm) load_gain<T, D>(t.w, a.w_f32, sub, w);
+  Walk at;
+  at.first(a, share, mine, full, lane);
+  Walk ahead = at;
+  int ahead_row = 0, ahead_unit = 0;
+  const T* xp = nullptr;
+  auto fetch = [&]() {
+    if (ahead.more()) {
+      if (ahead.it == 0) {
+        const int b = ahead.token / a.N, n = ahead.token - b * a.N;
+        xp = static_cast<const T*>(t.x) + b * t.sb + n * t.sn;
+        if (ahead.pos >= 0) copy_angles<T, D, kInter>(angles_at + ahead_unit * 4 * kStep, a.cos_t, a.sin_t, ahead.pos, sub);
+        ahead_unit = ahead_unit + 1 == R::kStages ? 0 : ahead_unit + 1;
+      }
+      const int h = (ahead.group + ahead.it) * kRows + lane / kLanes;
+      if (ahead.pos >= 0 && h < nh) copy_row<D>(rows_at + ahead_row * R::kRow * kStep, xp + h * t.sh, sub);
+      if (++ahead.it == ahead.its) ahead.next(a, share, lane);
+    }
+    ahead_row = ahead_row + 1 == R::kStages ? 0 : ahead_row + 1;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < R::kStages - 1; ++i) fetch();
+  int row_slot = 0, unit_slot = 0;
+  while (at.more()) {
+    T* o0 = static_cast<T*>(t.out) + static_cast<size_t>(at.token) * nh * D;
+    Coef k;
+    for (; at.it < at.its; ++at.it) {
+      fetch();
+      copies_wait<R::kStages - 1>();
+      if (at.it == 0) {
+        float2 c[4], s[4];
+        lds_angles(angles_at + unit_slot * 4 * kStep, c, s);
+        make_coef<kInter, kNorm>(c, s, w, k);
+        unit_slot = unit_slot + 1 == R::kStages ? 0 : unit_slot + 1;
+      }
+      const uint32_t src = rows_at + row_slot * R::kRow * kStep;
+      row_slot = row_slot + 1 == R::kStages ? 0 : row_slot + 1;
+      const int h = (at.group + at.it) * kRows + lane / kLanes;
+      Raw<T> raw;
+      float2 o[8];
+      lds_row(src, raw);  // whatever is there, where the position is padding
+      turn_row<D, kNorm, kInter>(raw, at.pos, k, a.eps, o);
+      if (h < nh) store_row<D>(o0 + static_cast<size_t>(h) * D, sub, o);
+    }
+    at.next(a, share, lane);
+  }
+  copies_wait<0>();
+}
+
+// The backward: each warp has its own running sum of the gain's gradient; a block writes
+// the sum of its warps to partial[block][d].  The registers that the gradient needs leave
+// room for 12 warps on an SM, whose own loads would keep only 24 KB in flight.
+template <typename T, int D, bool kNorm, bool kInter>
+__global__ void __launch_bounds__(kWarps * 32, 3) rope_bwd_kernel(const RopeArgs a) {
+  using R = Ring<T, kNorm ? 2 : 1>;
+  extern __shared__ __align__(16) uint8_t ring[];
+  constexpr int kLanes = D / 16;
+  constexpr int kRows = 32 / kLanes;
+  constexpr int kStep = R::kStep;
+  wait_for_previous_kernel();
+  const int lane = lane_id(), warp = warp_id();
+  const int sub = lane % kLanes;
+  const bool is_q = static_cast<int>(blockIdx.x) < a.q_blocks;
+  const int first = is_q ? blockIdx.x : blockIdx.x - a.q_blocks;
+  const int blocks = is_q ? a.q_blocks : static_cast<int>(gridDim.x) - a.q_blocks;
+  const int nh = is_q ? a.H : a.Hkv;
+  const RopeTensor& t = is_q ? a.q : a.k;
+  Shares share;
+  const unsigned int warps = blocks * kWarps, mine = first * kWarps + warp;
+  const int full = give_shares(share, a, is_q ? a.q_groups : a.k_groups, mine, warps);
   const uint32_t rows_at = smem_u32(ring) + threadIdx.x * 16;
   const uint32_t angles_at = rows_at + R::kStages * R::kPieces * kStep;
   float2 w[8], acc[8];
@@ -480,7 +600,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_bwd_kernel(const RopeArgs
 
   // the copies of one iteration, as one group (which may be empty)
   Walk at;
-  at.first(a, share, mine, static_cast<int>(full), lane);
+  at.first(a, share, mine, full, lane);
   Walk ahead = at;
   int ahead_row = 0, ahead_unit = 0;  // slots
   const T* gp = nullptr;
@@ -491,25 +611,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_bwd_kernel(const RopeArgs
         const int b = ahead.token / a.N, n = ahead.token - b * a.N;
         gp = static_cast<const T*>(t.g) + b * t.gb + n * t.gn;
         xp = static_cast<const T*>(t.x) + b * t.sb + n * t.sn;
-        if (ahead.pos >= 0) {
-          const size_t row = static_cast<size_t>(ahead.pos) * (D / 2);
-          const uint32_t dst = angles_at + ahead_unit * 4 * kStep;
-          if constexpr (kInter && sizeof(T) == 4) {  // as load_angles
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int at = feature<T, D>(2 * k, sub) / 2;
-              copy8_l1(dst + (k >> 1) * kStep + (k & 1) * 8, a.cos_t + row + at);
-              copy8_l1(dst + (2 + (k >> 1)) * kStep + (k & 1) * 8, a.sin_t + row + at);
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 4; k += 2) {
-              const int at = kInter ? feature<T, D>(2 * k, sub) / 2 : feature<T, D>(k, sub);
-              copy16_l1(dst + (k >> 1) * kStep, a.cos_t + row + at);
-              copy16_l1(dst + (2 + (k >> 1)) * kStep, a.sin_t + row + at);
-            }
-          }
-        }
+        if (ahead.pos >= 0) copy_angles<T, D, kInter>(angles_at + ahead_unit * 4 * kStep, a.cos_t, a.sin_t, ahead.pos, sub);
         ahead_unit = ahead_unit + 1 == R::kStages ? 0 : ahead_unit + 1;
       }
       const int h = (ahead.group + ahead.it) * kRows + lane / kLanes;
@@ -534,12 +636,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_bwd_kernel(const RopeArgs
       fetch();
       copies_wait<R::kStages - 1>();  // the oldest group has arrived
       if (at.it == 0) {
-        const uint32_t src = angles_at + unit_slot * 4 * kStep;
-        const float4 c0 = lds_f4(src), c1 = lds_f4(src + kStep), s0 = lds_f4(src + 2 * kStep), s1 = lds_f4(src + 3 * kStep);
-        c[0] = make_float2(c0.x, c0.y), c[1] = make_float2(c0.z, c0.w);
-        c[2] = make_float2(c1.x, c1.y), c[3] = make_float2(c1.z, c1.w);
-        s[0] = make_float2(s0.x, s0.y), s[1] = make_float2(s0.z, s0.w);
-        s[2] = make_float2(s1.x, s1.y), s[3] = make_float2(s1.z, s1.w);
+        lds_angles(angles_at + unit_slot * 4 * kStep, c, s);
         unit_slot = unit_slot + 1 == R::kStages ? 0 : unit_slot + 1;
       }
       const uint32_t src = rows_at + row_slot * R::kPieces * kStep;
@@ -640,10 +737,15 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__
 
 template <typename T, int D, bool kNorm, bool kInter>
 cudaError_t launch_fwd_k(const RopeArgs& a, cudaStream_t s) {
-  const dim3 grid((a.tokens + kWarps - 1) / kWarps, a.q_groups + a.k_groups);
-  constexpr int kMany = sizeof(T) == 2 ? 4 : 2;  // registers
-  if (a.per >= 4) return launch_behind(rope_fwd_kernel<T, D, kNorm, kInter, kMany>, grid, dim3(kWarps * 32), 0, s, a);
-  return launch_behind(rope_fwd_kernel<T, D, kNorm, kInter, kMany / 2>, grid, dim3(kWarps * 32), 0, s, a);
+  if (a.blocks == 0) {
+    const dim3 grid((a.tokens + kWarps - 1) / kWarps, a.q_groups + a.k_groups);
+    return launch_behind(rope_fwd_kernel<T, D, kNorm, kInter>, grid, dim3(kWarps * 32), 0, s, a);
+  }
+  constexpr int kBytes = Ring<T, 1>::kBytes;
+  const cudaError_t e =
+      cudaFuncSetAttribute(rope_fwd_rounds_kernel<T, D, kNorm, kInter>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+  if (e != cudaSuccess) return e;
+  return launch_behind(rope_fwd_rounds_kernel<T, D, kNorm, kInter>, dim3(a.blocks), dim3(kWarps * 32), kBytes, s, a);
 }
 
 template <typename T, int D>
@@ -655,7 +757,7 @@ cudaError_t launch_fwd_d(const RopeArgs& a, cudaStream_t s) {
 
 template <typename T, int D, bool kNorm, bool kInter>
 cudaError_t launch_bwd_k(const RopeArgs& a, cudaStream_t s) {
-  constexpr int kBytes = BwdRing<T, D, kNorm>::kBytes;
+  constexpr int kBytes = Ring<T, kNorm ? 2 : 1>::kBytes;
   const cudaError_t e =
       cudaFuncSetAttribute(rope_bwd_kernel<T, D, kNorm, kInter>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (e != cudaSuccess) return e;

@@ -195,6 +195,25 @@ def test_tensors_beyond_32_bit_offsets():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,H,Hkv,d,N", [(BF, 33, 7, 128, 20001), (BF, 4, 1, 64, 40009), (F32, 9, 9, 64, 45007)])
+def test_long_rows_equal_their_pieces(dtype, H, Hkv, d, N):
+    """Rows do not depend on one another: one call over many positions (hundreds of MB: other shares of a warp)
+    and calls over a few hundred each write the same bits, forward and dx."""
+    need_gpu()
+    q, k, cos, sin, w, pos, gq, gk = _case(dtype, 1, N, H, Hkv, d, True, False, True, True, F32, seed=31, rows=4000)
+    qo, ko = fa.qk_norm_rope(q, k, cos, sin, w[0], w[1], pos)
+    dq, dk, _, _ = fa.qk_norm_rope_bwd(q, k, cos, sin, gq, gk, w[0], w[1], pos)
+    for lo in list(range(0, N, 7919)) + [N - 301]:
+        at = slice(lo, lo + 301)
+        a, b = fa.qk_norm_rope(q[:, at], k[:, at], cos, sin, w[0], w[1], pos[:, at].contiguous())
+        assert torch.equal(a, qo[:, at]) and torch.equal(b, ko[:, at])
+        a, b, _, _ = fa.qk_norm_rope_bwd(q[:, at], k[:, at], cos, sin, gq[:, at], gk[:, at], w[0], w[1],
+                                         pos[:, at].contiguous())
+        assert torch.equal(a, dq[:, at]) and torch.equal(b, dk[:, at])
+    assert fa.last_device_status()[0] == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("inter", [False, True])
 def test_gradient_against_differences_of_the_kernel(inter):
     """Central differences of the fp32 forward itself.  Step 2^-7: the forward's error, 2^-20 of
