@@ -829,9 +829,13 @@ int fa_decode_paged(const void* Q, const void* K_cache, const void* V_cache, con
 namespace {
 
 constexpr int kRopeBlockWarps = 4;
-constexpr int kRopeFwdBlocks = 148 * 4;  // resident together
-constexpr int kRopeBwdBlocks = 148 * 3;
-constexpr int kRopeRound = 8;            // row groups (of 512 / d heads) of a warp in one round
+constexpr int kRopeBwdBlocks = 148 * 3;  // resident together
+constexpr int kRopePairs = 148 * 5 * 4 * 2;  // row groups (of 512 / d heads) of the warps resident together, two each
+// Row groups of a warp in one round.  Backward, bf16 d128: B4 N8192 H32 + 8 160 us with 4, 166 with
+// 8; B1 N16384 H32 + 32 130 and 133; d64 B8 N4096 H32 + 32 129 and 128.  Forward: B1 N4096 H64 + 8
+// 25.8 and 25.5, N2048 H32 + 8 8.5 and 7.8 (a position's start costs it more).
+constexpr int kRopeFwdRound = 8;
+constexpr int kRopeBwdRound = 4;
 
 bool aligned_strides(const long long* s, int dtype) {
   const long long m = dtype == FA_BF16 ? 8 : 4;  // 16 bytes
@@ -935,13 +939,14 @@ int fa_qk_norm_rope(const void* Q, const void* K, const void* q_weight, const vo
   RopeArgs a = rope_args(Q, K, q_weight, k_weight, cos_table, sin_table, positions, Q_out, K_out, B, N, H, Hkv, d,
                                q_strides, k_strides, table_rows, eps, interleaved, weight_dtype, st->status);
   const long long groups = static_cast<long long>(a.tokens) * (a.q_groups + a.k_groups);
-  if (groups >= kRopeFwdBlocks * kRopeBlockWarps * kRopeRound) {
-    // From one full round on, bf16 d128: B1 N2048 H32 + 8 (20480 groups) 8.5 us against 9.3 by
-    // pairs; d64 B4 N1001 H16 + 4 (12012 groups) 6.6 against 5.7.  Rounds of half the size from
-    // 400 MB on: B1 N15000 H32 + 32 (492 MB) 80 us against 88, B4 N8192 H32 + 8 (671 MB) 111
-    // against 116; B2 N8192 H32 + 8 (336 MB) 57.5 against 56.2, B1 N4096 H64 + 8 27.5 against 26.
+  if (groups >= kRopePairs) {
+    // B1 H32 + 8 d128 bf16: 5120 groups (N512) 3.5 us against 3.2 by pairs; 7000 (N700) 4.0
+    // against 4.5, 20480 (N2048) 7.7 against 9.3.  From 256 MB on three blocks per SM, because
+    // memory takes more requests in flight badly: B4 N8192 H32 + 8 (671 MB) 111 us against 122 with
+    // four, B1 N16384 H32 + 32 (537 MB) 86 against 97, B2 N8192 H32 + 8 (336 MB) 57 against 60;
+    // B1 N4096 H64 + 8 (151 MB) 27.4 against 25.5.
     const double bytes = 2.0 * a.tokens * (H + Hkv) * d * (dtype == FA_FP32 ? 4 : 2);
-    rope_rounds(&a, bytes < 400e6 ? kRopeRound : kRopeRound / 2, kRopeFwdBlocks);
+    rope_rounds(&a, kRopeFwdRound, bytes < 256e6 ? 148 * 4 : 148 * 3);
   } else {  // pairs of groups, a warp each
     a.q_groups = (a.q_groups + 1) / 2;
     a.k_groups = (a.k_groups + 1) / 2;
@@ -985,7 +990,7 @@ int fa_qk_norm_rope_bwd(const void* Q, const void* K, const void* q_weight, cons
   a.k.g = dK_out;
   set_strides(dq_out_strides, N, H, d, &a.q.gb, &a.q.gn, &a.q.gh);
   set_strides(dk_out_strides, N, Hkv, d, &a.k.gb, &a.k.gn, &a.k.gh);
-  if (!empty) rope_rounds(&a, kRopeRound, kRopeBwdBlocks);
+  if (!empty) rope_rounds(&a, kRopeBwdRound, kRopeBwdBlocks);
   a.partial = static_cast<float*>(workspace);
   a.dwq = dq_weight;
   a.dwk = dk_weight;

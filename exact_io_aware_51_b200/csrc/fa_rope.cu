@@ -23,9 +23,9 @@
 // pairs), each output is rounded once.
 //
 // Measured on a B200 (GPU time), d = 128, bf16: forward B1 N16384 H32 + 32 (537 MB) 86
-// us, 6.3 TB/s; B1 N4096 H64 + 8 out of a packed projection (151 MB) 26 us, 5.8 TB/s;
+// us, 6.2 TB/s; B1 N4096 H64 + 8 out of a packed projection (151 MB) 25.4 us, 5.9 TB/s;
 // backward B1 N16384 H32 + 32 (805 MB) 131 us with the gains' sums, 6.1 TB/s.
-// fp32: B2 N4096 H32 + 8 forward (335 MB) 59 us, 5.7 TB/s; backward (503 MB) 86 us, 5.9
+// fp32: B2 N4096 H32 + 8 forward (335 MB) 58 us, 5.8 TB/s; backward (503 MB) 86 us, 5.9
 // TB/s (130 us with a lane's 8 features of a half side by side: 32-byte steps).
 #include <cuda_bf16.h>
 
@@ -257,8 +257,8 @@ __device__ __forceinline__ int checked_position(const RopeArgs& a, int pos, int 
 
 // one row of the forward: every lane of the warp comes here, its row valid or not
 template <int D, bool kNorm, bool kInter, typename T>
-__device__ __forceinline__ void turn_row(const Raw<T>& raw, int pos, const Coef& k, float eps, float2 (&o)[8]) {
-  if (pos >= 0) {
+__device__ __forceinline__ void turn_row(const Raw<T>& raw, bool place, const Coef& k, float eps, float2 (&o)[8]) {
+  if (place) {  // not padding
     float2 x[8];
     unpack(raw, x);
     float r = 1.f;
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 && !kInter ? 5 : 4
     if (u && pair * 2 * kRows + kRows >= nh) break;  // no row of the second group
     if (u >= kAhead) load(u);
     float2 o[8];
-    turn_row<D, kNorm, kInter>(raw[u], pos, k, a.eps, o);
+    turn_row<D, kNorm, kInter>(raw[u], pos >= 0, k, a.eps, o);
     if (h0 + u * kRows < nh) store_row<D>(o0 + static_cast<size_t>(h0 + u * kRows) * D, sub, o);
   }
 }
@@ -326,9 +326,8 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 && !kInter ? 5 : 4
 // iterations wait in shared memory, written by asynchronous copies into slots of the
 // lane's own (no barrier).
 // ---------------------------------------------------------------------------
-// kTensors rows per iteration (x; or g and x).  Three stages, measured at B1 N16384 H32 +
-// 32 d128 bf16: backward 131 us (2: 135; 4: 143, more streams than memory likes; 1% better
-// on smaller ones at best); forward 86 (2: 94, 4: 86), B2 N8192 H32 + 8 56 (2: 60, 4: 62).
+// kTensors rows per iteration (x; or g and x).  Three stages against two, bf16 d128:
+// backward B1 N4096 H64 + 8 39.4 us and 42.4, forward 25.5 and 27.9.
 template <typename T, int kTensors>
 struct Ring {
   static constexpr int kStages = 3;
@@ -381,8 +380,8 @@ __device__ __forceinline__ void copy_row(uint32_t dst, const T* p, int sub) {
 // A warp's walk over row groups, counted through all positions (fewer than 2^32: B N H d
 // < 2^40).  In rounds, every warp takes the next `per` groups, so that the GPU reads one
 // stretch of memory at a time; what is left for no full round is cut into equal ranges.
-// Without the cut, whole ranges of a position: B1 N8192 H40 + 40 d128 101 us for 81.  One
-// range per warp, and no rounds: H32 + 32 N16384 139 us for 131, d64 133 for 125.
+// Backward, without the cut (whole ranges of a position): B1 N8192 H40 + 40 d128 101 us for
+// 81.  One range per warp and no rounds: H32 + 32 N16384 139 us for 131, d64 133 for 125.
 struct Shares {
   unsigned int groups;          // of a position
   unsigned int per, step;       // of a warp's range, of a round
@@ -394,21 +393,28 @@ struct Walk {
   int rounds;             // full rounds after that one; -1: the rest is given out, too
   int it, its;            // iteration, iterations at this position
   int group;              // first group at this position
-  int token, ntoken;      // position in [0, B N): this one, the next range's first
-  int pos, coming;        // the caller's: this one's, the next one's (asked for one ahead)
+  int token, b, n;        // position in [0, B N): b N + n
+  int ntoken, nb, nn;     // the next one
+  int pos, coming;        // the caller's positions of both (the next one's asked for ahead)
   __device__ __forceinline__ bool more() const { return g < end; }
-  static __device__ __forceinline__ int raw_position(const RopeArgs& a, int tok) {
-    return a.positions ? a.positions[tok] : tok % a.N;
+  static __device__ __forceinline__ int raw_position(const RopeArgs& a, int tok, int n) {
+    return a.positions ? a.positions[tok] : n;
   }
   __device__ __forceinline__ void open(const RopeArgs& a, const Shares& w, int raw, int lane) {  // g < end
     pos = checked_position(a, raw, lane);
     its = static_cast<int>(min(end - g, w.groups - group));
     it = 0;
     if (end - g > static_cast<unsigned int>(its)) {
-      coming = raw_position(a, token + 1);
+      ntoken = token + 1;
+      const bool wrap = n + 1 == a.N;
+      nb = b + wrap;
+      nn = wrap ? 0 : n + 1;
+      coming = raw_position(a, ntoken, nn);
     } else if (ng < nend) {
       ntoken = static_cast<int>(ng / w.groups);
-      coming = raw_position(a, ntoken);
+      nb = ntoken / a.N;
+      nn = ntoken - nb * a.N;
+      coming = raw_position(a, ntoken, nn);
     }
   }
   // the range after [ng, nend)
@@ -431,25 +437,35 @@ struct Walk {
     after(w);
     if (!more()) return;
     token = static_cast<int>(g / w.groups);
+    b = token / a.N;
+    n = token - b * a.N;
     group = static_cast<int>(g - static_cast<unsigned int>(token) * w.groups);
-    open(a, w, raw_position(a, token), lane);
+    open(a, w, raw_position(a, token, n), lane);
   }
   __device__ __forceinline__ void next(const RopeArgs& a, const Shares& w, int lane) {
     g += its;
-    if (more()) {
-      ++token;
-      group = 0;
-    } else {
+    const bool jump = !more();
+    if (jump) {
       g = ng;
       end = nend;
       if (!more()) return;
       after(w);
-      token = ntoken;
-      group = static_cast<int>(g - static_cast<unsigned int>(token) * w.groups);
     }
+    token = ntoken;
+    b = nb;
+    n = nn;
+    group = jump ? static_cast<int>(g - static_cast<unsigned int>(token) * w.groups) : 0;
     open(a, w, coming, lane);
   }
 };
+
+// An iteration on its way: where its row goes (this lane's), and what it is
+template <typename T>
+struct Coming {
+  T* out;
+  unsigned int is;
+};
+constexpr unsigned int kLive = 1, kPlace = 2, kFresh = 4, kHead = 8;  // there is one; not padding; new angles; a row
 
 // warp `mine`'s shares of the row groups; returns the full rounds
 __device__ __forceinline__ int give_shares(Shares& s, const RopeArgs& a, int groups, unsigned int mine,
@@ -494,11 +510,10 @@ __device__ __forceinline__ void lds_angles(uint32_t src, float2 (&c)[4], float2 
   s[2] = make_float2(s1.x, s1.y), s[3] = make_float2(s1.z, s1.w);
 }
 
-// The forward at 4 blocks per SM (120 registers; 5 spill).  Against warps with one position
-// each and four rows loaded ahead, bf16 d128: B1 N4096 H64 + 8 26.0 us (27.3), B2 N8192 H32 +
-// 8 56.2 (60), B1 N8192 H40 + 40 55.8 (60.8), B1 N16384 H32 + 32 85.8 (84.4); fp32: B2
-// N4096 H32 + 8 58.6 (60.7), d64 B4 N2048 H16 + 16 22 (28.4).  The norm stands before the
-// rotation in turn_row: the other order took 10% more at N16384.
+// The forward at 3 or 4 blocks per SM (120 registers; 5 spill).  Against warps with one
+// position each and four rows loaded ahead, bf16 d128: B1 N2048 H32 + 8 7.7 us (9.3), B1
+// N4096 H64 + 8 25.4 (27.3), B2 N8192 H32 + 8 57 (60), B1 N8192 H40 + 40 55.6 (60.8), B1
+// N16384 H32 + 32 86 (84.4); d64 B4 N4096 H16 + 16 23.4 (29.7).
 template <typename T, int D, bool kNorm, bool kInter>
 __global__ void __launch_bounds__(kWarps * 32, 4) rope_fwd_rounds_kernel(const RopeArgs a) {
   using R = Ring<T, 1>;
@@ -521,51 +536,60 @@ __global__ void __launch_bounds__(kWarps * 32, 4) rope_fwd_rounds_kernel(const R
   const uint32_t angles_at = rows_at + R::kStages * R::kRow * kStep;
   float2 w[8];
   if (kNorm) load_gain<T, D>(t.w, a.w_f32, sub, w);
-  Walk at;
-  at.first(a, share, mine, full, lane);
-  Walk ahead = at;
-  int ahead_row = 0, ahead_unit = 0;
+  Walk ahead;
+  ahead.first(a, share, mine, full, lane);
+  int ahead_row = 0, ahead_unit = 0, h = 0;  // slots; head of this lane's row
   const T* xp = nullptr;
+  T* op = nullptr;
+  // the copies of one iteration, as one group (which may be empty)
   auto fetch = [&]() {
+    Coming<T> c = {nullptr, 0};
     if (ahead.more()) {
+      c.is = kLive;
       if (ahead.it == 0) {
-        const int b = ahead.token / a.N, n = ahead.token - b * a.N;
-        xp = static_cast<const T*>(t.x) + b * t.sb + n * t.sn;
+        c.is |= kFresh;
+        h = ahead.group * kRows + lane / kLanes;
+        xp = static_cast<const T*>(t.x) + ahead.b * t.sb + ahead.n * t.sn + h * t.sh;
+        op = static_cast<T*>(t.out) + (static_cast<size_t>(ahead.token) * nh + h) * D;
         if (ahead.pos >= 0) copy_angles<T, D, kInter>(angles_at + ahead_unit * 4 * kStep, a.cos_t, a.sin_t, ahead.pos, sub);
         ahead_unit = ahead_unit + 1 == R::kStages ? 0 : ahead_unit + 1;
       }
-      const int h = (ahead.group + ahead.it) * kRows + lane / kLanes;
-      if (ahead.pos >= 0 && h < nh) copy_row<D>(rows_at + ahead_row * R::kRow * kStep, xp + h * t.sh, sub);
+      if (ahead.pos >= 0) c.is |= kPlace;
+      if (h < nh) c.is |= kHead;
+      if (ahead.pos >= 0 && h < nh) copy_row<D>(rows_at + ahead_row * R::kPieces * kStep, xp, sub);
+      c.out = op;
+      h += kRows;
+      xp += kRows * t.sh;
+      op += kRows * D;
       if (++ahead.it == ahead.its) ahead.next(a, share, lane);
     }
     ahead_row = ahead_row + 1 == R::kStages ? 0 : ahead_row + 1;
     asm volatile("cp.async.commit_group;" ::: "memory");
+    return c;
   };
+  Coming<T> line[R::kStages - 1];
 #pragma unroll
-  for (int i = 0; i < R::kStages - 1; ++i) fetch();
+  for (int i = 0; i < R::kStages - 1; ++i) line[i] = fetch();
   int row_slot = 0, unit_slot = 0;
-  while (at.more()) {
-    T* o0 = static_cast<T*>(t.out) + static_cast<size_t>(at.token) * nh * D;
-    Coef k;
-    for (; at.it < at.its; ++at.it) {
-      fetch();
-      copies_wait<R::kStages - 1>();
-      if (at.it == 0) {
-        float2 c[4], s[4];
-        lds_angles(angles_at + unit_slot * 4 * kStep, c, s);
-        make_coef<kInter, kNorm>(c, s, w, k);
-        unit_slot = unit_slot + 1 == R::kStages ? 0 : unit_slot + 1;
-      }
-      const uint32_t src = rows_at + row_slot * R::kRow * kStep;
-      row_slot = row_slot + 1 == R::kStages ? 0 : row_slot + 1;
-      const int h = (at.group + at.it) * kRows + lane / kLanes;
-      Raw<T> raw;
-      float2 o[8];
-      lds_row(src, raw);  // whatever is there, where the position is padding
-      turn_row<D, kNorm, kInter>(raw, at.pos, k, a.eps, o);
-      if (h < nh) store_row<D>(o0 + static_cast<size_t>(h) * D, sub, o);
+  Coef k;
+  while (line[0].is & kLive) {
+    const Coming<T> at = line[0];
+#pragma unroll
+    for (int i = 0; i < R::kStages - 2; ++i) line[i] = line[i + 1];
+    line[R::kStages - 2] = fetch();
+    copies_wait<R::kStages - 1>();  // the oldest group has arrived
+    if (at.is & kFresh) {
+      float2 c[4], s[4];
+      lds_angles(angles_at + unit_slot * 4 * kStep, c, s);
+      make_coef<kInter, kNorm>(c, s, w, k);
+      unit_slot = unit_slot + 1 == R::kStages ? 0 : unit_slot + 1;
     }
-    at.next(a, share, lane);
+    Raw<T> raw;
+    float2 o[8];
+    lds_row(rows_at + row_slot * R::kPieces * kStep, raw);  // whatever is there, where the position is padding
+    row_slot = row_slot + 1 == R::kStages ? 0 : row_slot + 1;
+    turn_row<D, kNorm, kInter>(raw, at.is & kPlace, k, a.eps, o);
+    if (at.is & kHead) store_row<D>(at.out, sub, o);
   }
   copies_wait<0>();
 }
@@ -598,86 +622,94 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_bwd_kernel(const RopeArgs
 #pragma unroll
   for (int j = 0; j < 8; ++j) acc[j] = make_float2(0.f, 0.f);
 
-  // the copies of one iteration, as one group (which may be empty)
-  Walk at;
-  at.first(a, share, mine, full, lane);
-  Walk ahead = at;
-  int ahead_row = 0, ahead_unit = 0;  // slots
+  Walk ahead;
+  ahead.first(a, share, mine, full, lane);
+  int ahead_row = 0, ahead_unit = 0, h = 0;  // slots; head of this lane's row
   const T* gp = nullptr;
   const T* xp = nullptr;
+  T* op = nullptr;
+  // the copies of one iteration, as one group (which may be empty)
   auto fetch = [&]() {
+    Coming<T> c = {nullptr, 0};
     if (ahead.more()) {
+      c.is = kLive;
       if (ahead.it == 0) {
-        const int b = ahead.token / a.N, n = ahead.token - b * a.N;
-        gp = static_cast<const T*>(t.g) + b * t.gb + n * t.gn;
-        xp = static_cast<const T*>(t.x) + b * t.sb + n * t.sn;
+        c.is |= kFresh;
+        h = ahead.group * kRows + lane / kLanes;
+        gp = static_cast<const T*>(t.g) + ahead.b * t.gb + ahead.n * t.gn + h * t.gh;
+        xp = static_cast<const T*>(t.x) + ahead.b * t.sb + ahead.n * t.sn + h * t.sh;
+        op = static_cast<T*>(t.out) + (static_cast<size_t>(ahead.token) * nh + h) * D;
         if (ahead.pos >= 0) copy_angles<T, D, kInter>(angles_at + ahead_unit * 4 * kStep, a.cos_t, a.sin_t, ahead.pos, sub);
         ahead_unit = ahead_unit + 1 == R::kStages ? 0 : ahead_unit + 1;
       }
-      const int h = (ahead.group + ahead.it) * kRows + lane / kLanes;
+      if (ahead.pos >= 0) c.is |= kPlace;
+      if (h < nh) c.is |= kHead;
       if (ahead.pos >= 0 && h < nh) {
         const uint32_t dst = rows_at + ahead_row * R::kPieces * kStep;
-        copy_row<D>(dst, gp + h * t.gh, sub);
-        if (kNorm) copy_row<D>(dst + R::kRow * kStep, xp + h * t.sh, sub);
+        copy_row<D>(dst, gp, sub);
+        if (kNorm) copy_row<D>(dst + R::kRow * kStep, xp, sub);
       }
+      c.out = op;
+      h += kRows;
+      gp += kRows * t.gh;
+      xp += kRows * t.sh;
+      op += kRows * D;
       if (++ahead.it == ahead.its) ahead.next(a, share, lane);
     }
     ahead_row = ahead_row + 1 == R::kStages ? 0 : ahead_row + 1;
     asm volatile("cp.async.commit_group;" ::: "memory");
+    return c;
   };
-
+  Coming<T> line[R::kStages - 1];
 #pragma unroll
-  for (int i = 0; i < R::kStages - 1; ++i) fetch();
+  for (int i = 0; i < R::kStages - 1; ++i) line[i] = fetch();
   int row_slot = 0, unit_slot = 0;
-  while (at.more()) {
-    T* o0 = static_cast<T*>(t.out) + static_cast<size_t>(at.token) * nh * D;
-    float2 c[4], s[4];
-    for (; at.it < at.its; ++at.it) {
-      fetch();
-      copies_wait<R::kStages - 1>();  // the oldest group has arrived
-      if (at.it == 0) {
-        lds_angles(angles_at + unit_slot * 4 * kStep, c, s);
-        unit_slot = unit_slot + 1 == R::kStages ? 0 : unit_slot + 1;
-      }
-      const uint32_t src = rows_at + row_slot * R::kPieces * kStep;
-      row_slot = row_slot + 1 == R::kStages ? 0 : row_slot + 1;
-      const int h = (at.group + at.it) * kRows + lane / kLanes;
-      const bool ok = h < nh;
-      float2 o[8];
+  float2 c[4], s[4];
+  while (line[0].is & kLive) {
+    const Coming<T> at = line[0];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = make_float2(0.f, 0.f);
-      if (at.pos >= 0) {  // what a lane without a row holds stays in its row's lanes
-        Raw<T> raw;
-        float2 g[8], gr[8];
-        lds_row(src, raw);
-        unpack(raw, g);
-        rotate_back<kInter>(g, c, s, gr);
-        if constexpr (!kNorm) {
+    for (int i = 0; i < R::kStages - 2; ++i) line[i] = line[i + 1];
+    line[R::kStages - 2] = fetch();
+    copies_wait<R::kStages - 1>();
+    if (at.is & kFresh) {
+      lds_angles(angles_at + unit_slot * 4 * kStep, c, s);
+      unit_slot = unit_slot + 1 == R::kStages ? 0 : unit_slot + 1;
+    }
+    const uint32_t src = rows_at + row_slot * R::kPieces * kStep;
+    row_slot = row_slot + 1 == R::kStages ? 0 : row_slot + 1;
+    float2 o[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = gr[j];
-        } else {
-          float2 x[8];
-          lds_row(src + R::kRow * kStep, raw);
-          unpack(raw, x);
-          const float r = row_rsqrt<D>(x, a.eps);
-          float2 dot = make_float2(0.f, 0.f), gx[8];
+    for (int j = 0; j < 8; ++j) o[j] = make_float2(0.f, 0.f);
+    if (at.is & kPlace) {  // what a lane without a row holds stays in its row's lanes
+      Raw<T> raw;
+      float2 g[8], gr[8];
+      lds_row(src, raw);
+      unpack(raw, g);
+      rotate_back<kInter>(g, c, s, gr);
+      if constexpr (!kNorm) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            gx[j] = fmul2(gr[j], x[j]);
-            dot = ffma2(gx[j], w[j], dot);
-          }
-          const float m = row_sum<D>(dot.x + dot.y) * (1.f / D) * r * r * r;
-          const float2 r2 = make_float2(r, r), m2 = make_float2(-m, -m);
+        for (int j = 0; j < 8; ++j) o[j] = gr[j];
+      } else {
+        float2 x[8];
+        lds_row(src + R::kRow * kStep, raw);
+        unpack(raw, x);
+        const float r = row_rsqrt<D>(x, a.eps);
+        float2 dot = make_float2(0.f, 0.f), gx[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            if (ok) acc[j] = ffma2(gx[j], r2, acc[j]);
-            o[j] = ffma2(fmul2(gr[j], w[j]), r2, fmul2(x[j], m2));
-          }
+        for (int j = 0; j < 8; ++j) {
+          gx[j] = fmul2(gr[j], x[j]);
+          dot = ffma2(gx[j], w[j], dot);
+        }
+        const float m = row_sum<D>(dot.x + dot.y) * (1.f / D) * r * r * r;
+        const float2 r2 = make_float2(r, r), m2 = make_float2(-m, -m);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (at.is & kHead) acc[j] = ffma2(gx[j], r2, acc[j]);
+          o[j] = ffma2(fmul2(gr[j], w[j]), r2, fmul2(x[j], m2));
         }
       }
-      if (ok) store_row<D>(o0 + static_cast<size_t>(h) * D, sub, o);
     }
-    at.next(a, share, lane);
+    if (at.is & kHead) store_row<D>(at.out, sub, o);
   }
   copies_wait<0>();
 
