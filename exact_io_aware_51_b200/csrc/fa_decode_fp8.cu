@@ -30,15 +30,18 @@
 //   * P goes from the accumulator layout to the operand layout with movmatrix.
 // Rounding: q is scaled by a power of two per head so that its largest element is in
 // [2^7, 2^8), exact in f16 down to 2^-24 of it.  P times the V scales is rounded to
-// f16 (the running maximum of the V scales' exponents is taken out, like m); sums,
-// maxima and statistics are fp32.
+// f16, with a power of two near the V scales taken out, like m; where the scales that a warp
+// meets are too far apart for f16 it is split into two bf16 terms.  Sums, maxima and
+// statistics are fp32.
 //
 // Measured on a B200 (GPU time): 64 sequences of 512 to 8192 positions, 64 heads on 8,
 // d = 128, 16-token pages, 632 MB: 101 us, 6.25 TB/s (95% of a copy's 6.57); one
 // sequence of 100000, 206 MB: 40 us, of which 8 us are the start, the last merge and the
 // join.  Beyond 8 heads a K/V head, and for d = 64, the consumers' latency and not the
 // memory bounds it (64 heads on 4: 67 us for 290 MB; with Q's fragments in registers the
-// two blocks of positions had to go one after the other: 77 us).  What did not pay:
+// two blocks of positions had to go one after the other: 77 us).  The two bf16 terms: 115 us
+// for the 100 of the 64 sequences where each begins with a V row of zeros (one warp in
+// four walks its sequences that way), 70 for 61 at d = 64.  What did not pay:
 //   * a grid of (sequence, chunk) with two CTAs per SM, codes converted with integer
 //     shifts (7 operations a word): 161 us;
 //   * e4m3 operands for S^T with m16n8k32 and q split in two: 129 us (the instruction is
@@ -72,6 +75,15 @@ constexpr int kThreads = (kConsumers + 1) * 32;
 // units): p <= 2^kLazy, and P * 2^(15 - kLazy) stays inside f16.
 constexpr float kLazy = 6.f;
 constexpr int kPShift = 9;
+// P times the V scales goes to f16, in a unit of 2^kVUp times the largest V scale of its first 32 rows,
+// as long as every scale that a warp meets in a sequence is at most that unit and at least 2^-kVSpan
+// of it.  What a product loses is then below 2^(kVSpan - 34) of its own V row, however small that
+// is beside the others.  From the first scale outside on the products are sums of two bf16 terms,
+// which have fp32's range, and the unit follows the largest scale (up to 2^32, so that the range serves
+// both ways).
+constexpr int kVUp = 4;
+constexpr int kVSpan = 10;
+constexpr int kVCap = 127 + 32;
 constexpr int kBarBytes = 192;
 
 template <int D, int NT>
@@ -146,6 +158,19 @@ __device__ __forceinline__ bool elect_one() {
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(r));
   return r != 0;
+}
+__device__ __forceinline__ void mma_bf16(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// an f16 pair that holds e4m3 values as a bf16 pair (exact)
+__device__ __forceinline__ uint32_t bf16_of_f16(uint32_t x) {
+  const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&x));
+  return pack_bf16x2(v.x, v.y);
 }
 // codes 0, 2 and codes 1, 3 of a word as f16 pairs
 __device__ __forceinline__ void f16_pairs(uint32_t w, uint32_t& even, uint32_t& odd) {
@@ -480,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
       sync_consumers();
     }
     float o[D / 16][NT][4];
-    float mt[NT][2], mq[NT][2], lazy[NT][2];  // reference in t; mq = reference in x (0 while there is none)
+    float mt[NT][2], mq[NT][2];  // reference in t; mq = reference in x (0 while there is none)
     float2 l[NT];
 #pragma unroll
     for (int c = 0; c < D / 16; ++c)
@@ -493,10 +518,10 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
       for (int i = 0; i < 2; ++i) {
         mt[nt][i] = -INFINITY;
         mq[nt][i] = 0.f;
-        lazy[nt][i] = fminf(kLazy / qf[nt][i], 1e30f);
       }
     }
-    int eref = 0;  // the largest V scale byte so far: P is multiplied by 2^(byte - eref)
+    int unit = -1000;   // V scale byte of the sums' unit: P is multiplied by 2^(byte - unit); negative: no position yet
+    bool wide = false;  // two bf16 terms
     int bad = 0;
 
     bool ok = true;
@@ -521,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
       const bool edge = key0 + kTileKeys > kend || key0 < lo;
       if (edge) {
         const int first = key0 + warp * kWarpKeys;
-        if (first + lane >= kend || first + lane < lo) vbyte = 0;
+        if (first + lane >= kend || first + lane < lo) vbyte = unit;
         for (int i = lane; i < kWarpKeys * (D / 16); i += 32) {
           const int r = i / (D / 16);
           if (first + r >= kend || first + r < lo) st_shared_v4(vs + unit_off<D>(r, i % (D / 16)), 0u, 0u, 0u, 0u);
@@ -575,18 +600,23 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
           }
       }
       float mx[NT][2];
-      bool grow = vbyte > eref;
+      bool grow = static_cast<uint32_t>(unit - vbyte) > kVSpan;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           mx[nt][i] = fmaxf(fmaxf(s[0][nt][i], s[0][nt][2 + i]), fmaxf(s[1][nt][i], s[1][nt][2 + i]));
-          grow |= mx[nt][i] > mt[nt][i] + lazy[nt][i];
+          grow |= (mx[nt][i] - mt[nt][i]) * qf[nt][i] > kLazy;
         }
       if (__any_sync(0xffffffffu, grow)) {
-        const int en = max(eref, static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<uint32_t>(vbyte))));
-        const float eal = __uint_as_float(static_cast<uint32_t>(max(0, 127 + eref - en)) << 23);
-        eref = en;
+        const int top = __reduce_max_sync(0xffffffffu, vbyte);
+        if (unit < 0 && top >= 0) unit = min(top + kVUp, kVCap);
+        float eal = 1.f;
+        wide |= __any_sync(0xffffffffu, vbyte >= 0 && static_cast<uint32_t>(unit - vbyte) > kVSpan);
+        if (wide && min(top, kVCap) > unit) {
+          eal = __uint_as_float(static_cast<uint32_t>(max(0, 127 + unit - min(top, kVCap))) << 23);
+          unit = min(top, kVCap);
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -609,39 +639,79 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
             }
           }
       }
-      // P^T as the B operand: p * 2^(V byte - eref) * 2^kPShift in f16, transposed
-      const float vf = __uint_as_float(static_cast<uint32_t>(max(0, vbyte - eref + 127 + kPShift)) << 23);
-      uint32_t pb[2][NT][2];
+      // P^T as the B operand, transposed: p * 2^(V byte - unit) * 2^kPShift
+      if (!wide) {
+        uint32_t pb[2][NT][2];
+        const float vf = __uint_as_float(static_cast<uint32_t>(vbyte - unit + 127 + kPShift) << 23);
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          const float f = __shfl_sync(0xffffffffu, vf, u * 16 + hh * 8 + kg);
+          for (int hh = 0; hh < 2; ++hh) {
+            const float f = __shfl_sync(0xffffffffu, vf, u * 16 + hh * 8 + kg);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const float2 p = make_float2(ex2(fmaf(s[u][nt][2 * hh], qf[nt][0], -mq[nt][0])),
-                                         ex2(fmaf(s[u][nt][2 * hh + 1], qf[nt][1], -mq[nt][1])));
-            l[nt] = fadd2(l[nt], p);
-            const float2 pv = fmul2(p, make_float2(f, f));
-            pb[u][nt][hh] = movmatrix_t(pack_f16x2(pv.x, pv.y));
+            for (int nt = 0; nt < NT; ++nt) {
+              const float2 p = make_float2(ex2(fmaf(s[u][nt][2 * hh], qf[nt][0], -mq[nt][0])),
+                                           ex2(fmaf(s[u][nt][2 * hh + 1], qf[nt][1], -mq[nt][1])));
+              l[nt] = fadd2(l[nt], p);
+              const float2 pv = fmul2(p, make_float2(f, f));
+              pb[u][nt][hh] = movmatrix_t(pack_f16x2(pv.x, pv.y));
+            }
+          }
+        // O^T += V^T P^T: one ldmatrix.trans covers 16 positions x 32 features
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t r[4];
+            ldsm_x4_t(vs + unit_off<D>(u * 16 + (mi & 1) * 8 + key_of<D>(rr), 2 * cc + (mi >> 1)), r);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t a0, a1, a2, a3;
+              f16_pairs(r[2 * i], a0, a1);
+              f16_pairs(r[2 * i + 1], a2, a3);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_f16(o[2 * cc + i][nt], a0, a1, a2, a3, pb[u][nt][0], pb[u][nt][1]);
+            }
+          }
+      } else {
+        // the same in bf16 (a code is exact in it, too), once for P and once for what its rounding left;
+        // one block of 16 positions at a time, because unrolled it made the f16 branch spill (5% slower)
+        const float vf = vbyte == 255 ? __uint_as_float(0x7fc00000u)
+                                      : __uint_as_float(static_cast<uint32_t>(max(0, vbyte - unit + 127 + kPShift)) << 23);
+#pragma unroll 1
+        for (int step = 0; step < 4; ++step) {
+          const bool second = step & 2, rest = step & 1;  // positions 16 to 31; P's rounding error
+          uint32_t w[NT][2];
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const float f = __shfl_sync(0xffffffffu, vf, (second ? 16 : 0) + hh * 8 + kg);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const float2 p = make_float2(ex2(fmaf(second ? s[1][nt][2 * hh] : s[0][nt][2 * hh], qf[nt][0], -mq[nt][0])),
+                                           ex2(fmaf(second ? s[1][nt][2 * hh + 1] : s[0][nt][2 * hh + 1], qf[nt][1], -mq[nt][1])));
+              if (!rest) l[nt] = fadd2(l[nt], p);
+              const float2 pv = fmul2(p, make_float2(f, f));
+              uint32_t b = pack_bf16x2(pv.x, pv.y);
+              if (rest) b = pack_bf16x2(pv.x - __uint_as_float(b << 16), pv.y - __uint_as_float(b & 0xffff0000u));
+              w[nt][hh] = movmatrix_t(b);
+            }
+          }
+#pragma unroll
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t r[4];
+            ldsm_x4_t(vs + unit_off<D>((second ? 16 : 0) + (mi & 1) * 8 + key_of<D>(rr), 2 * cc + (mi >> 1)), r);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t a0, a1, a2, a3;
+              f16_pairs(r[2 * i], a0, a1);
+              f16_pairs(r[2 * i + 1], a2, a3);
+              a0 = bf16_of_f16(a0), a1 = bf16_of_f16(a1), a2 = bf16_of_f16(a2), a3 = bf16_of_f16(a3);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_bf16(o[2 * cc + i][nt], a0, a1, a2, a3, w[nt][0], w[nt][1]);
+            }
           }
         }
-      // O^T += V^T P^T: one ldmatrix.trans covers 16 positions x 32 features
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int cc = 0; cc < D / 32; ++cc) {
-          uint32_t r[4];
-          ldsm_x4_t(vs + unit_off<D>(u * 16 + (mi & 1) * 8 + key_of<D>(rr), 2 * cc + (mi >> 1)), r);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t a0, a1, a2, a3;
-            f16_pairs(r[2 * i], a0, a1);
-            f16_pairs(r[2 * i + 1], a2, a3);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(o[2 * cc + i][nt], a0, a1, a2, a3, pb[u][nt][0], pb[u][nt][1]);
-          }
-        }
+      }
       if (edge) fence_proxy_async_smem();  // the next TMA write of the stage follows the zeros
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->empty[st]);
@@ -677,8 +747,8 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
       for (int i = 0; i < 2; ++i) {
         // P's 2^kPShift and the V exponent go out here.  A warp that saw nothing has zeros (or
         // NaN, if all it saw was NaN) and takes them as they are.
-        const float f = scalbnf(ex2(mq[nt][i] - head_max(nt * 8 + 2 * t4 + i)), eref - 127 - kPShift);
-        of[nt][i] = eref == 255 ? __uint_as_float(0x7fc00000u) : mt[nt][i] == -INFINITY ? 1.f : f;
+        const float f = scalbnf(ex2(mq[nt][i] - head_max(nt * 8 + 2 * t4 + i)), unit - 127 - kPShift);
+        of[nt][i] = mt[nt][i] == -INFINITY ? 1.f : f;
       }
     // head and features of this thread in every slice (threads past the last head have none)
     constexpr int kPer = 4;

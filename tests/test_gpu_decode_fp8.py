@@ -153,6 +153,68 @@ def test_growing_scores_and_scales(H):
         args = (q, *args[1:])
 
 
+def _planted(x, v, H, d, P, seed):
+    """Decode arguments of one sequence whose head scores are the rows x [n] (on the e4m3 grid times a power of
+    two) and whose V rows are v [n, d]: q is the first unit vector, K holds x in that feature."""
+    n = len(x)
+    g = torch.Generator().manual_seed(seed)
+    pages = (n + P - 1) // P
+    table = torch.randperm(pages, generator=g).to(torch.int32).view(1, pages)
+    k, w = np.zeros((pages, P, 1, d)), np.zeros((pages, P, 1, d))
+    for j in range(n):
+        k[int(table[0, j // P]), j % P, 0, 0] = x[j]
+        w[int(table[0, j // P]), j % P, 0] = v[j]
+    kc, kb = S.quantise_rows(k)
+    vc, vb = S.quantise_rows(w)
+    sc = np.ascontiguousarray(np.stack([np.moveaxis(kb, 1, 2), np.moveaxis(vb, 1, 2)], axis=2))
+    q = torch.zeros((1, H, d), dtype=torch.bfloat16)
+    q[:, :, 0] = 1
+    return q, torch.from_numpy(kc), torch.from_numpy(vc), torch.from_numpy(sc), table, torch.tensor([n], dtype=torch.int32)
+
+
+def _unlike_rows(n, d, what, seed):
+    """Scores (natural logarithms of the probabilities but for a constant) and V rows in which few rows are of
+    a size far from the others'."""
+    rng = np.random.default_rng(seed)
+    x, v = rng.integers(0, 2, n) * -1.0, rng.standard_normal((n, d))
+    if what.startswith("unlikely"):       # one large row that its probability makes small again, or nothing
+        bits, nats = {"unlikely28": (28, 22.0), "unlikely40": (40, 40.0), "unlikely100": (100, 72.0)}[what]
+        v[n // 3] *= 2.0 ** bits
+        x[n // 3] = -nats
+    elif what == "sparse":                # a likely large row that is zero in most features
+        v[n // 3] *= 2.0 ** 34
+        v[n // 3, 5:] = 0
+    elif what == "later":                 # the second half larger by what its probability is smaller
+        v[n // 2:] *= 2.0 ** 30
+        x[n // 2:] -= 20.0
+    elif what == "earlier":
+        v[:n // 2] *= 2.0 ** 30
+        x[:n // 2] -= 20.0
+    elif what == "sink":                  # nearly all probability on a row of zeros
+        v[0] = 0
+        x[1:] -= 24.0
+    else:
+        assert what == "huge and small"
+        v *= 2.0 ** -60
+        v[n // 3, :3] = 2.0 ** 100
+        v[n // 3, 3:] = 0
+    return x, v
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("what", ["unlikely28", "unlikely40", "unlikely100", "sparse", "later", "earlier", "sink",
+                                  "huge and small"])
+@pytest.mark.parametrize("n,H,d", [(20, 4, 128), (700, 8, 64), (700, 16, 128), (300, 12, 64), (5000, 8, 128)])
+def test_v_rows_of_very_different_size(what, n, H, d):
+    """The bound of every other case holds where few V rows are of a size far from the others': unlikely and large,
+    large in few features, zeros that take the probability; in one tile, in several, and in several ranges."""
+    need_gpu()
+    args = _planted(*_unlike_rows(n, d, what, seed=n), H, d, 16, seed=17)
+    for window in (None, n - 2):
+        o, lse = _run(args, scale=1.0, window_left=window)
+        _check(args, o, lse, 1.0, window)
+
+
 @pytest.mark.gpu
 def test_nan_rows_reach_the_heads_that_see_them():
     need_gpu()
