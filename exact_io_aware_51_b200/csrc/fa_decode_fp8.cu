@@ -75,6 +75,9 @@ constexpr int kThreads = (kConsumers + 1) * 32;
 // units): p <= 2^kLazy, and P * 2^(15 - kLazy) stays inside f16.
 constexpr float kLazy = 6.f;
 constexpr int kPShift = 9;
+// Scores are held with q's power of two still in them, up to 2^24 times K's scale (up to 2^120): another
+// 2^-kKShift keeps the largest finite, and the smallest (K's scale 2^-126) above fp32's subnormals' end.
+constexpr int kKShift = 20;
 // P times the V scales goes to f16, in a unit of 2^kVUp times the largest V scale of its first 32 rows,
 // as long as every scale that a warp meets in a sequence is at most that unit and at least 2^-kVSpan
 // of it.  What a product loses is then below 2^(kVSpan - 34) of its own V row, however small that
@@ -455,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
     // (its 16-byte units t4 and, for d = 128, t4 + 4): q = (qh + ql / 16) 2^(e - 134)
     uint32_t qb[NT][D / 16][2];  // kSharedQ: on their way to the merge's place, [nt][k step][lane]
     const uint32_t q_at = smem_u32(smem + C::kOffMerge) + lane * 8;
-    float qf[NT][2];  // heads 2 t4, 2 t4 + 1: scale_log2 * 2^(e - 134)
+    float qf[NT][2];  // heads 2 t4, 2 t4 + 1: scale_log2 * 2^(e - 134 + kKShift)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const bool have = nt * 8 + g < gv;
@@ -489,10 +492,10 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
       for (int i = 0; i < 2; ++i) {
         const int eh = __shfl_sync(0xffffffffu, e, (2 * t4 + i) * 4);
         // kept finite and positive, so that a hidden score stays -inf
-        qf[nt][i] = fminf(fmaxf(scalbnf(a.scale_log2, eh - 134), 1.2e-38f), 3e38f);
+        qf[nt][i] = fminf(fmaxf(scalbnf(a.scale_log2, eh - 134 + kKShift), 1.2e-38f), 3e38f);
       }
     }
-    // scores are held as t = <q, k> with q's power of two still in it: x = t qf
+    // scores are held as t = <q, k> 2^-kKShift with q's power of two still in it: x = t qf
     if constexpr (C::kSharedQ) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -538,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
       bad |= *reinterpret_cast<volatile int*>(&bars->bad[st]);
 
       // this lane's position: factor of K, byte of V
-      const float kf = scale_of(lds_u8(sc));
+      const float kf = scale_of(lds_u8(sc)) * (1.f / (1 << kKShift));
       int vbyte = static_cast<int>(lds_u8(sc + R));
 
       // positions outside [lo, kend) are hidden, whatever their bytes are; their V rows are

@@ -216,6 +216,26 @@ def test_v_rows_of_very_different_size(what, n, H, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d,H", [(128, 8), (64, 32)])
+def test_small_queries_on_large_keys_and_the_reverse(d, H):
+    """Scores of ordinary size whose factors are up to 2^115 away from it."""
+    need_gpu()
+    args = _make(2, H, 2, d, 16, [300, 129], seed=18, poison=False)
+    q, kc, vc, sc, table, sl = args
+    q = torch.where(q.abs() < 2.0 ** -4, torch.tensor(2.0 ** -4, dtype=q.dtype), q)  # no subnormals below
+    want = _run((q, *args[1:]), scale=0.2)
+    for e in (115, 60, -60, -110):
+        s2 = sc.clone()
+        s2[:, :, 0] = (sc[:, :, 0].int() + e).to(torch.uint8)
+        got = (q * 2.0 ** -e, kc, vc, s2, table, sl)
+        assert torch.equal(got[0].double(), q.double() * 2.0 ** -e)
+        o, lse = _run(got, scale=0.2)
+        _check(got, o, lse, 0.2)
+        if e > -110:  # only powers of two have moved (at -110 the smallest scores are subnormal on the way)
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.gpu
 def test_nan_rows_reach_the_heads_that_see_them():
     need_gpu()
     args = _make(2, 8, 2, 128, 16, [300, 300], seed=10)
