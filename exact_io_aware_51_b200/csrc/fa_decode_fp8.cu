@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
       sync_consumers();
     }
     float o[D / 16][NT][4];
-    float mt[NT][2], mq[NT][2];  // reference in t; mq = reference in x (0 while there is none)
+    float mt[NT][2], m0[NT][2];  // reference, in t; m0: the same, but 0 while there is none
     float2 l[NT];
 #pragma unroll
     for (int c = 0; c < D / 16; ++c)
@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         mt[nt][i] = -INFINITY;
-        mq[nt][i] = 0.f;
+        m0[nt][i] = 0.f;
       }
     }
     int unit = -1000;   // V scale byte of the sums' unit: P is multiplied by 2^(byte - unit); negative: no position yet
@@ -631,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
             v = fmaxf(v, mt[nt][i]);
             const float al = (v == -INFINITY) ? 1.f : ex2((mt[nt][i] - v) * qf[nt][i]);
             mt[nt][i] = v;
-            mq[nt][i] = (v == -INFINITY) ? 0.f : v * qf[nt][i];
+            m0[nt][i] = (v == -INFINITY) ? 0.f : v;
             if (i == 0) l[nt].x *= al;
             else l[nt].y *= al;
             const float oal = al * eal;
@@ -642,6 +642,12 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
             }
           }
       }
+      // the reference is taken off before the factor: a product's rounding, 2^-24 of the score, would reach the
+      // exponent, and from scores of 2^28 on leave f16
+      auto probability = [&](float2 t, int nt) {
+        const float2 x = fmul2(fadd2(t, make_float2(-m0[nt][0], -m0[nt][1])), make_float2(qf[nt][0], qf[nt][1]));
+        return make_float2(ex2(x.x), ex2(x.y));
+      };
       // P^T as the B operand, transposed: p * 2^(V byte - unit) * 2^kPShift
       if (!wide) {
         uint32_t pb[2][NT][2];
@@ -653,8 +659,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
             const float f = __shfl_sync(0xffffffffu, vf, u * 16 + hh * 8 + kg);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const float2 p = make_float2(ex2(fmaf(s[u][nt][2 * hh], qf[nt][0], -mq[nt][0])),
-                                           ex2(fmaf(s[u][nt][2 * hh + 1], qf[nt][1], -mq[nt][1])));
+              const float2 p = probability(make_float2(s[u][nt][2 * hh], s[u][nt][2 * hh + 1]), nt);
               l[nt] = fadd2(l[nt], p);
               const float2 pv = fmul2(p, make_float2(f, f));
               pb[u][nt][hh] = movmatrix_t(pack_f16x2(pv.x, pv.y));
@@ -690,8 +695,8 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
             const float f = __shfl_sync(0xffffffffu, vf, (second ? 16 : 0) + hh * 8 + kg);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const float2 p = make_float2(ex2(fmaf(second ? s[1][nt][2 * hh] : s[0][nt][2 * hh], qf[nt][0], -mq[nt][0])),
-                                           ex2(fmaf(second ? s[1][nt][2 * hh + 1] : s[0][nt][2 * hh + 1], qf[nt][1], -mq[nt][1])));
+              const float2 p = probability(make_float2(second ? s[1][nt][2 * hh] : s[0][nt][2 * hh],
+                                                       second ? s[1][nt][2 * hh + 1] : s[0][nt][2 * hh + 1]), nt);
               if (!rest) l[nt] = fadd2(l[nt], p);
               const float2 pv = fmul2(p, make_float2(f, f));
               uint32_t b = pack_bf16x2(pv.x, pv.y);
@@ -732,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
         v += __shfl_xor_sync(0xffffffffu, v, 8);
         v += __shfl_xor_sync(0xffffffffu, v, 16);
         if (g == 0) {
-          mw[warp * 16 + nt * 8 + 2 * t4 + i] = mt[nt][i] == -INFINITY ? -INFINITY : mq[nt][i];
+          mw[warp * 16 + nt * 8 + 2 * t4 + i] = mt[nt][i] == -INFINITY ? -INFINITY : __fmul_rn(mt[nt][i], qf[nt][i]);
           lw[warp * 16 + nt * 8 + 2 * t4 + i] = v;
         }
       }
@@ -750,7 +755,8 @@ __global__ void __launch_bounds__(kThreads, Cfg8<D, NT>::kCtas)
       for (int i = 0; i < 2; ++i) {
         // P's 2^kPShift and the V exponent go out here.  A warp that saw nothing has zeros (or
         // NaN, if all it saw was NaN) and takes them as they are.
-        const float f = scalbnf(ex2(mq[nt][i] - head_max(nt * 8 + 2 * t4 + i)), unit - 127 - kPShift);
+        // The product is rounded as the one in mw was (an fma would not round it).
+        const float f = scalbnf(ex2(__fmul_rn(m0[nt][i], qf[nt][i]) - head_max(nt * 8 + 2 * t4 + i)), unit - 127 - kPShift);
         of[nt][i] = mt[nt][i] == -INFINITY ? 1.f : f;
       }
     // head and features of this thread in every slice (threads past the last head have none)

@@ -236,6 +236,25 @@ def test_small_queries_on_large_keys_and_the_reverse(d, H):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("n,H,d", [(6, 8, 128), (6, 32, 64), (900, 8, 64)])
+@pytest.mark.parametrize("e", [24, 40, 118])
+def test_scores_so_large_that_one_row_takes_all(n, H, d, e):
+    """Scores of 2^e, far apart: the output is the V row of the largest.  LSE is that score, scale log2(e) rounded
+    once, its product with the score, and ln 2 times that, once each: 4 * 2^-24 of it."""
+    need_gpu()
+    rng = np.random.default_rng(n)
+    x = rng.choice([1.0, 1.25, -3.5, 2.0, 0.0], n) * 2.0 ** e
+    x[n - 4] = 3.0 * 2.0 ** e
+    args = _planted(x, rng.standard_normal((n, d)), H, d, 16, seed=19)
+    o, lse = _run(args, scale=0.25)
+    V = S.dequantise_cache(*args[1:4])[1]
+    want = torch.from_numpy(V[int(args[4][0, (n - 4) // 16]), (n - 4) % 16, 0]).to(torch.bfloat16)
+    for h in range(H):
+        assert torch.equal(o.cpu()[0, h], want)
+        assert abs(float(lse[0, h]) - 0.75 * 2.0 ** e) <= 2.0 ** -22 * 0.75 * 2.0 ** e
+
+
+@pytest.mark.gpu
 def test_nan_rows_reach_the_heads_that_see_them():
     need_gpu()
     args = _make(2, 8, 2, 128, 16, [300, 300], seed=10)
