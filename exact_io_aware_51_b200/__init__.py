@@ -591,8 +591,8 @@ def rope_tables(positions: int, d: int, base: float = 10000.0, device="cuda"):
 
 def qk_norm_rope(q, k, cos, sin, q_weight=None, k_weight=None, positions=None, eps: float = 1e-6,
                  interleaved: bool = False):
-    """Differentiable ``qk_norm_rope_fwd`` (gradients of q, k and the gains; the tables get none): the step before
-    ``attention``.  As with any autograd function, capture its backward into a CUDA graph only while no eager graph of
+    """Differentiable ``qk_norm_rope_fwd`` (gradients of q, k and the gains; the tables get none; no forward-mode
+    derivative): the step before ``attention``.  As with any autograd function, capture its backward into a CUDA graph only while no eager graph of
     the same leaves is alive (PyTorch accumulates into a leaf on the stream of the graph that saw it first)."""
     return _native().norm_rope(q, k, cos, sin, q_weight, k_weight, positions, eps, interleaved)
 

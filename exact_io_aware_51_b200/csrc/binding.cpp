@@ -445,6 +445,11 @@ Rope rope_of(PyObject* const* a) {  // q, k, cos, sin, q_weight, k_weight, posit
 PyObject* py_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {  // rope_of, with autograd
   return guarded(n, 9, [&] {
     Rope r = rope_of(a);
+    if (c10::AutogradState::get_tls_state().get_fw_grad_mode()) {  // tangents need no requires_grad
+      for (const Tensor* t : {&r.q, &r.k, &r.wq, &r.wk, &r.cos, &r.sin})
+        TORCH_CHECK_NOT_IMPLEMENTED(!t->defined() || !t->_fw_grad(/*level=*/0).defined(),
+                                    "qk_norm_rope has no forward-mode derivative");
+    }
     auto wants = [](const Tensor& t) { return t.defined() && t.requires_grad(); };
     if (at::GradMode::is_enabled() && (wants(r.q) || wants(r.k) || wants(r.wq) || wants(r.wk))) {
       const auto out = RopeFunction::apply(r.q, r.k, RopeFunction::given(r.wq), RopeFunction::given(r.wk), r.cos, r.sin,

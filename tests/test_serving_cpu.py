@@ -264,6 +264,27 @@ def test_python_norm_rope_refusals(L):
         f(q, k, c, c, interleaved=torch.ones(2))
 
 
+def test_forward_mode_derivatives_are_refused(L):
+    """There is none, and a tangent must not be lost: fa.attention refuses it, too."""
+    import torch.autograd.forward_ad as fwad
+
+    q = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16)
+    k = torch.zeros(2, 3, 2, 64, dtype=torch.bfloat16)
+    c, w = torch.zeros(8, 32), torch.zeros(64, dtype=torch.bfloat16)
+    given = {"q": q, "k": k, "cos": c, "sin": c, "q_weight": w, "k_weight": w}
+    with fwad.dual_level():
+        for name, t in given.items():
+            args = {**given, name: fwad.make_dual(t, torch.ones_like(t))}
+            with pytest.raises(NotImplementedError, match="forward-mode"):
+                fa.qk_norm_rope(**args)
+            with torch.no_grad(), pytest.raises(NotImplementedError, match="forward-mode"):
+                fa.qk_norm_rope(**args)
+            with pytest.raises(ValueError, match="CUDA"), fwad._set_fwd_grad_enabled(False):
+                fa.qk_norm_rope(**args)
+        with pytest.raises(ValueError, match="CUDA"):
+            fa.qk_norm_rope(**given)
+
+
 def test_python_cache_refusals(L):
     kc = torch.zeros(5, 8, 2, 64, dtype=torch.uint8)
     sc = torch.zeros(5, 2, 2, 8, dtype=torch.uint8)
