@@ -105,6 +105,15 @@ void check_out(const Tensor& t, at::IntArrayRef shape, at::ScalarType type, cons
                     name, " must be a contiguous ", type, " tensor of shape ", shape, " on ", like.device());
 }
 
+// A caller's tensor that a call writes: autograd has to know, so that a graph that saved it for its
+// backward refuses to run, as after any in-place operation
+void will_write(const Tensor& t, const char* name) {
+  if (!t.defined()) return;
+  TORCH_CHECK_VALUE(!(at::GradMode::is_enabled() && t.requires_grad()), name,
+                    " is written in place and must not be one that requires a gradient");
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 // a dense tensor on like's device, without the dispatcher's 0.5 us
 Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
   return at::detail::empty_cuda(shape, type, like.device(), std::nullopt);
@@ -113,6 +122,7 @@ Tensor fresh(at::IntArrayRef shape, at::ScalarType type, const Tensor& like) {
 Tensor out_or_new(const Tensor& given, at::IntArrayRef shape, at::ScalarType type, const Tensor& like, const char* name) {
   if (!given.defined()) return fresh(shape, type, like);
   check_out(given, shape, type, like, name);
+  will_write(given, name);
   return given;
 }
 
@@ -196,6 +206,7 @@ struct Rope {
     Tensor dq = fresh(q.sizes(), q.scalar_type(), q), dk = fresh(k.sizes(), q.scalar_type(), q), dwq, dwk, ws = workspace;
     size_t bytes = 0;
     if (wq.defined()) {
+      will_write(ws, "workspace");
       dwq = fresh(wq.sizes(), wq.scalar_type(), q);
       dwk = fresh(wk.sizes(), wk.scalar_type(), q);
       if (!ws.defined()) ws = fresh({static_cast<int64_t>(api.norm_rope_ws(d))}, at::kByte, q);
@@ -322,6 +333,9 @@ void cache_append(const Tensor& k, const Tensor& v, Cache c, const Tensor& count
   }
   const Strides ks(k, "k"), vs(v, "v");
   const int N = as_int(k.size(1), "the positions");
+  will_write(c.k, "k_cache");
+  will_write(c.v, "v_cache");
+  will_write(c.scale, "kv_scale");
   Here here(c.k);
   check_status(call_unlocked([&] {
                  return api.append(ptr(k), ptr(v), mut(c.k), mut(c.v), mut(c.scale), c.table_ptr(), c.lengths_ptr(),
@@ -361,6 +375,7 @@ std::pair<Tensor, Tensor> decode(const Tensor& q, Cache c, double scale, int win
   Here here(q);
   Tensor o = out_or_new(out, q.sizes(), at::kBFloat16, q, "out"), ws = workspace;
   Tensor l = out_or_new(lse, {c.B, H}, at::kFloat, q, "lse");
+  will_write(ws, "workspace");
   if (!ws.defined()) {
     const size_t need = api.decode_ws(c.B, H, c.Hkv, c.d, c.page_size, c.max_pages, window);
     if (need) ws = fresh({static_cast<int64_t>(need)}, at::kByte, q);

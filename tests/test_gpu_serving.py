@@ -118,6 +118,57 @@ def test_prompt_then_captured_decode_steps(fp8):
 
 
 @pytest.mark.gpu
+def test_autograd_sees_what_the_calls_write():
+    """A graph that saved a buffer for its backward refuses to run once a call has written it; a buffer that is part
+    of a graph itself is refused; an inference tensor is written as any other."""
+    need_gpu()
+    bf = {"dtype": torch.bfloat16, "device": "cuda"}
+    cos, sin = fa.rope_tables(8, 64)
+    q, k = torch.randn(2, 3, 4, 64, **bf), torch.randn(2, 3, 2, 64, **bf)
+    table = torch.arange(4, dtype=torch.int32, device="cuda").view(2, 2)
+    lens = torch.full((2,), 3, dtype=torch.int32, device="cuda")
+    zero = torch.zeros_like(lens)
+
+    def pools(dtype):
+        c = [torch.zeros(4, 8, 2, 64, dtype=dtype, device="cuda") for _ in range(2)]
+        return c if dtype == torch.bfloat16 else [*c, torch.full((4, 2, 2, 8), 127, dtype=torch.uint8, device="cuda")]
+
+    kv, kv8 = pools(torch.bfloat16), pools(torch.uint8)
+    calls = [  # the buffers written, the call
+        ([torch.empty_like(q), torch.empty_like(k)],
+         lambda b: fa.qk_norm_rope_fwd(q, k, cos, sin, q_out=b[0], k_out=b[1])),
+        (pools(torch.bfloat16), lambda b: fa.cache_append(k, k, b[0], b[1], table, zero)),
+        (pools(torch.uint8), lambda b: fa.cache_append(k, k, b[0], b[1], table, zero, kv_scale=b[2])),
+        ([torch.empty_like(k), torch.empty_like(k)],
+         lambda b: fa.cache_read(*kv, table, lens, 3, k_out=b[0], v_out=b[1])),
+        ([torch.empty(2, 4, 64, **bf), torch.empty(2, 4, device="cuda")],
+         lambda b: fa.decode_paged_fp8(q[:, 0].contiguous(), *kv8, table, lens, out=b[0], lse=b[1])),
+    ]
+    for bufs, call in calls:
+        before = [b._version for b in bufs]
+        call(bufs)
+        assert all(b._version > v for b, v in zip(bufs, before))
+        for i, b in enumerate(bufs):
+            if not b.is_floating_point():
+                continue
+            x = torch.ones((), dtype=b.dtype, device="cuda", requires_grad=True)
+            y = (b * x).sum()
+            call(bufs)
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                y.backward()
+            with pytest.raises(ValueError, match="requires? a gradient"):
+                call([b.detach().requires_grad_(True) if j == i else other for j, other in enumerate(bufs)])
+            with torch.no_grad():
+                call([b.detach().requires_grad_(True) if j == i else other for j, other in enumerate(bufs)])
+        with torch.inference_mode():
+            call([b.clone() for b in bufs])
+    ws = torch.empty(fa.lib().fa_qk_norm_rope_workspace_size(64), dtype=torch.uint8, device="cuda")
+    w, v = torch.ones(64, device="cuda"), ws._version
+    fa.qk_norm_rope_bwd(q, k, cos, sin, q, k, w, w, workspace=ws)
+    assert ws._version > v
+
+
+@pytest.mark.gpu
 def test_two_graphs_and_an_eager_call_do_not_share_scratch():
     """Split decodes captured twice, replayed on two streams at once beside an eager one: each has partials of its own."""
     need_gpu()
