@@ -119,23 +119,25 @@ __device__ __forceinline__ void store_row(float* p, int sub, const float2 (&x)[8
 // The 8 (c, s) of this lane's pairs, laid out for rotate(): Half: cs[j] belongs to
 // the features x[j] and x[4 + j]; interleaved: to the pair x[2j], x[2j + 1] split
 // as c[j].x for x[2j], c[j].y for x[2j + 1].
+// Ordinary loads: the launch overlaps the end of the kernel before, which may write the tables, and what
+// griddepcontrol.wait orders are not the loads of the read-only path.
 template <typename T, int D, bool kInter>
-__device__ __forceinline__ void load_angles(const float* __restrict__ cos_t, const float* __restrict__ sin_t, int pos,
-                                            int sub, float2 (&c)[4], float2 (&s)[4]) {
+__device__ __forceinline__ void load_angles(const float* cos_t, const float* sin_t, int pos, int sub, float2 (&c)[4],
+                                            float2 (&s)[4]) {
   const size_t row = static_cast<size_t>(pos) * (D / 2);
   if constexpr (kInter && sizeof(T) == 4) {  // a run holds two pairs: two neighbouring angles
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int at = feature<T, D>(2 * k, sub) / 2;
-      c[k] = __ldg(reinterpret_cast<const float2*>(cos_t + row + at));
-      s[k] = __ldg(reinterpret_cast<const float2*>(sin_t + row + at));
+      c[k] = *reinterpret_cast<const float2*>(cos_t + row + at);
+      s[k] = *reinterpret_cast<const float2*>(sin_t + row + at);
     }
   } else {
 #pragma unroll
     for (int k = 0; k < 4; k += 2) {  // four neighbouring angles each
       const int at = kInter ? feature<T, D>(2 * k, sub) / 2 : feature<T, D>(k, sub);
-      const float4 vc = __ldg(reinterpret_cast<const float4*>(cos_t + row + at));
-      const float4 vs = __ldg(reinterpret_cast<const float4*>(sin_t + row + at));
+      const float4 vc = *reinterpret_cast<const float4*>(cos_t + row + at);
+      const float4 vs = *reinterpret_cast<const float4*>(sin_t + row + at);
       c[k] = make_float2(vc.x, vc.y);
       c[k + 1] = make_float2(vc.z, vc.w);
       s[k] = make_float2(vs.x, vs.y);
@@ -742,7 +744,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_bwd_kernel(const RopeArgs
 // dw = sum of the blocks' partial sums, in 64 bits and in a fixed order: grid (q or k,
 // 32 features), 32 x 32 threads of one feature and every 32nd block each
 template <int D>
-__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__ partial, int q_blocks, int blocks,
+__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* partial, int q_blocks, int blocks,
                                                        void* dwq, void* dwk, int w_f32) {
   __shared__ double sums[32][33];
   const int f = lane_id(), part = warp_id();

@@ -387,6 +387,43 @@ def test_nan_and_inf_stay_in_their_rows():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N", [3, 2000])
+@pytest.mark.parametrize("captured", [False, True])
+def test_tables_rewritten_right_before_the_call(N, captured):
+    """The kernels come up while the one before ends: each call reads the tables, gains and rows as that one left
+    them, also where the call before it had read the old ones."""
+    need_gpu()
+    q, k, cos, sin, w, pos, gq, gk = _case(BF, 1, N, 8, 2, 128, True, False, False, False, F32, seed=25)
+    cos0, sin0, q0 = cos.clone(), sin.clone(), q.clone()
+    steps = []
+    for _ in range(4):
+        cos0, sin0, q0 = -sin0, cos0, q0 * -0.5
+        steps.append((cos0, sin0, q0, fa.qk_norm_rope_fwd(q0, k, cos0, sin0, w[0], w[1]),
+                      fa.qk_norm_rope_bwd(q0, k, cos0, sin0, gq, gk, w[0], w[1])))
+
+    def run():
+        out = []
+        for c, s, x, _, _ in steps:
+            cos.copy_(c), sin.copy_(s), q.copy_(x)
+            out.append(fa.qk_norm_rope_fwd(q, k, cos, sin, w[0], w[1]))
+            cos.copy_(c), sin.copy_(s)
+            out.append(fa.qk_norm_rope_bwd(q, k, cos, sin, gq, gk, w[0], w[1]))
+        return out
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = run()
+        for _ in range(20):
+            graph.replay()
+    else:
+        for _ in range(20):
+            out = run()
+    for (_, _, _, fwd, bwd), a, b in zip(steps, out[0::2], out[1::2]):
+        assert all(torch.equal(x, y) for x, y in zip((*fwd, *bwd), (*a, *b)))
+
+
+@pytest.mark.gpu
 def test_captured_and_on_another_stream():
     """One graph of forward and backward, replayed on new inputs; and the calls on a side stream."""
     need_gpu()
