@@ -561,6 +561,10 @@ def _native():
     global _BINDING
     if _BINDING is None:
         L = lib()
+        from .build import BINDING, binding_is_current
+        if BINDING.exists() and not binding_is_current():
+            raise FAError(-6, f"{BINDING} was built for another PyTorch or Python; build it again with "
+                              "`python -m exact_io_aware_51_b200.build`")
         try:
             from . import _binding
         except ImportError as e:

@@ -52,9 +52,20 @@ def _deps():
             + [INCLUDE / "fa.h", pathlib.Path(__file__)])
 
 
+def binding_is_current() -> bool:
+    """Whether _binding.so names this PyTorch and this Python as those it was compiled against."""
+    return BINDING.exists() and _binding_tag().encode() in BINDING.read_bytes()
+
+
+def _binding_tag() -> str:
+    import torch
+
+    return f"binding for PyTorch {torch.__version__}, {sys.implementation.cache_tag};"
+
+
 def up_to_date() -> bool:
     libs = (LIB, PROBE_LIB, DEBUG_LIB, BINDING)
-    if not all(p.exists() for p in libs):
+    if not all(p.exists() for p in libs) or not binding_is_current():
         return False
     t = min(p.stat().st_mtime for p in libs)
     return all(p.stat().st_mtime <= t for p in _deps())
@@ -82,8 +93,8 @@ def _binding(verbose: bool) -> None:
     cuda = pathlib.Path(nvcc()).resolve().parents[1]
     tmp = BINDING.with_suffix(".so.tmp")
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", str(INCLUDE),
-           "-isystem", str(root / "include"), "-isystem", str(root / "include" / "torch" / "csrc" / "api" / "include"),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DFA_BINDING_TAG="{_binding_tag()}"',
+           "-I", str(INCLUDE), "-isystem", str(root / "include"), "-isystem", str(root / "include" / "torch" / "csrc" / "api" / "include"),
            "-isystem", sysconfig.get_paths()["include"], "-isystem", str(cuda / "include"), str(CSRC / "binding.cpp"),
            "-o", str(tmp), "-L", str(root / "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
            "-ltorch_python"]

@@ -559,7 +559,9 @@ PyMethodDef methods[] = {method("init", py_init),
                          method("cache_read", py_cache_read),
                          method("decode_paged_fp8", py_decode),
                          {nullptr, nullptr, 0, nullptr}};
-PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", "Calls of the operators around the attention (see binding.cpp).", -1, methods,
+// build.py looks for the tag in the file, so that another PyTorch's binding is neither kept nor loaded
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding",
+                      "Calls of the operators around the attention (see binding.cpp).\n" FA_BINDING_TAG, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -230,6 +230,22 @@ def test_decode_fp8_validation(L):
     assert size(1, 32, 8, 96, 16, 4096, -1) == 0 and size(1, 32, 8, 128, 16, 4096, -2) == 0
 
 
+# ---------------------------------------------------------------- the binding's build
+def test_binding_belongs_to_one_pytorch(L, monkeypatch):
+    """Under another PyTorch than it was compiled against it counts as out of date, and is not loaded."""
+    kc = torch.zeros(5, 8, 2, 64, dtype=torch.bfloat16)
+    bt, st = torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    assert fabuild.up_to_date()
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".other")
+    monkeypatch.setattr(fa, "_BINDING", None)
+    assert not fabuild.up_to_date()
+    with pytest.raises(fa.FAError, match="another PyTorch"):
+        fa.cache_read(kc, kc, bt, st, 4)
+    monkeypatch.undo()
+    with pytest.raises(ValueError, match="CUDA"):
+        fa.cache_read(kc, kc, bt, st, 4)
+
+
 # ---------------------------------------------------------------- refusals of the binding
 def test_python_norm_rope_refusals(L):
     q = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16)
