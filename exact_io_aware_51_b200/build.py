@@ -117,7 +117,6 @@ def build(force: bool = False, verbose: bool = False) -> pathlib.Path:
     with concurrent.futures.ThreadPoolExecutor(max_workers=len(jobs) + 1) as ex:
         binding = ex.submit(_binding, verbose)
         objs = dict(zip(jobs, ex.map(lambda j: _compile(CSRC / j[0], verbose, j[1]), jobs)))
-        binding.result()
     for lib, srcs, debug in ((LIB, SOURCES, False), (PROBE_LIB, PROBE_SOURCES, False), (DEBUG_LIB, SOURCES, True)):
         tmp = lib.with_suffix(".so.tmp")
         cmd = [nvcc(), *ARCH, "-shared", "-o", str(tmp), *(str(objs[(s, debug)]) for s in srcs), "-cudart", "static"]
@@ -125,6 +124,7 @@ def build(force: bool = False, verbose: bool = False) -> pathlib.Path:
         if r.returncode != 0:
             raise RuntimeError(f"link of {lib.name} failed:\n{r.stdout}\n{r.stderr}")
         os.replace(tmp, lib)
+    binding.result()  # the libraries do not need it
     return LIB
 
 

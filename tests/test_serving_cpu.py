@@ -246,6 +246,31 @@ def test_binding_belongs_to_one_pytorch(L, monkeypatch):
         fa.cache_read(kc, kc, bt, st, 4)
 
 
+def test_libraries_are_linked_where_the_binding_fails(tmp_path, monkeypatch):
+    """A C user needs no binding: what goes wrong with it is raised after the libraries are there."""
+    libs = {n: tmp_path / f"{n.lower()}.so" for n in ("LIB", "PROBE_LIB", "DEBUG_LIB")}
+    for n, p in libs.items():
+        monkeypatch.setattr(fabuild, n, p)
+    monkeypatch.setattr(fabuild, "BUILD", tmp_path / "_build")
+    monkeypatch.setattr(fabuild, "_compile", lambda src, verbose, debug=False: tmp_path / f"{src.stem}{debug}.o")
+
+    def linker(cmd, **kw):
+        out = cmd[cmd.index("-o") + 1]
+        assert "-shared" in cmd and all(x.endswith(".o") for x in cmd[cmd.index("-o") + 2:-2])
+        open(out, "w").close()
+        return fabuild.subprocess.CompletedProcess(cmd, 0, "", "")
+
+    def broken(verbose):
+        raise RuntimeError("no compiler for the binding")
+
+    monkeypatch.setattr(fabuild, "subprocess", type("S", (), {"run": staticmethod(linker),
+                                                              "CompletedProcess": fabuild.subprocess.CompletedProcess}))
+    monkeypatch.setattr(fabuild, "_binding", broken)
+    with pytest.raises(RuntimeError, match="no compiler"):
+        fabuild.build(force=True)
+    assert all(p.exists() for p in libs.values())
+
+
 # ---------------------------------------------------------------- refusals of the binding
 def test_python_norm_rope_refusals(L):
     q = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16)
