@@ -213,6 +213,111 @@ def test_long_rows_equal_their_pieces(dtype, H, Hkv, d, N):
     assert fa.last_device_status()[0] == 0
 
 
+def _dw_terms(x, cos, sin, pos, g, inter):
+    """gr x r of every row [B, N, heads, d] in float64, on the tensors' device (zeros where padding is)."""
+    x, g, d = x.double(), g.double(), x.shape[-1]
+    at = torch.arange(x.shape[1], device=x.device).expand(x.shape[:2]) if pos is None else pos.long()
+    c, s = (t.double()[at.clamp(min=0)][:, :, None] for t in (cos, sin))
+    a, b = (slice(0, d, 2), slice(1, d, 2)) if inter else (slice(0, d // 2), slice(d // 2, d))
+    gr = torch.empty_like(g)
+    gr[..., a], gr[..., b] = g[..., a] * c + g[..., b] * s, g[..., b] * c - g[..., a] * s
+    r = (x.square().mean(-1, keepdim=True) + 1e-6).rsqrt()
+    return torch.where((at >= 0)[:, :, None, None], gr * x * r, 0.0)
+
+
+def _sums(x, cos, sin, pos, g, inter):
+    """Sum and sum of magnitudes of the terms, a stretch of positions at a time."""
+    out = torch.zeros((2, x.shape[-1]), dtype=torch.float64, device=x.device)
+    for n in range(0, x.shape[1], 2048):
+        at = slice(n, n + 2048)
+        p = torch.arange(x.shape[1], device=x.device).expand(x.shape[:2]) if pos is None else pos
+        t = _dw_terms(x[:, at], cos, sin, p[:, at], g[:, at], inter)
+        out += torch.stack((t.sum((0, 1, 2)), t.abs().sum((0, 1, 2))))
+    return out
+
+
+def _depth(q, k):
+    """How many fp32 additions a term of a gain's gradient goes through, at most.  The rows of q and k go in
+    groups of 512 / d heads to 1776 resident warps (fewer where a warp would have less than two groups), by the
+    groups of a position and one more: at least half of the share that the groups alone would give.  A lane adds its
+    warp's groups one by one (a round of 4 and a rest more or less), then come the lanes of a feature (3), the
+    warps of a block (4), and 64 bits."""
+    n = 512 // q.shape[-1]
+    groups = q.shape[0] * q.shape[1] * ((q.shape[2] + n - 1) // n + (k.shape[2] + n - 1) // n)
+    return 2 * groups / 1776 + 5 + 3 + 4
+
+
+LONG = [(BF, 2, 37, 5, 3, 128, True), (BF, 2, 3001, 8, 4, 64, False), (BF, 1, 3301, 33, 5, 128, False),
+        (F32, 1, 3301, 33, 5, 128, True), (BF, 1, 20001, 33, 7, 128, False), (BF, 1, 40009, 4, 1, 64, True),
+        (F32, 1, 45007, 9, 9, 64, False), (BF, 4, 1001, 16, 4, 64, False)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("one_sign", [True, False])
+@pytest.mark.parametrize("dtype,B,N,H,Hkv,d,inter", LONG)
+def test_gain_gradients_to_the_depth_of_their_sums(dtype, B, N, H, Hkv, d, inter, one_sign):
+    """dw against a float64 sum, with 2^-24 for every fp32 addition that a term goes through (``_depth``), 32 for what
+    went into the term (the module's docstring counts fewer), and the last rounding.  With gradients
+    along the rotated rows all terms have one sign, so that a group of rows left out, or counted
+    twice, anywhere, is further off than that (in the calls over more than 10000 positions the groups of 16)."""
+    need_gpu()
+    q, k, cos, sin, w, pos, gq, gk = _case(dtype, B, N, H, Hkv, d, True, inter, True, True, F32, seed=26)
+    if one_sign:
+        gq, gk = fa.qk_norm_rope_fwd(q, k, cos, sin, positions=pos, interleaved=inter)
+    got = fa.qk_norm_rope_bwd(q, k, cos, sin, gq, gk, w[0], w[1], pos, interleaved=inter)[2:]
+    for x, g, dw in ((q, gq, got[0]), (k, gk, got[1])):
+        ref, mag = _sums(x, cos, sin, pos, g, inter)
+        tol = 2.0 ** -24 * ((_depth(q, k) + 32) * mag + ref.abs())
+        assert bool(((dw.double() - ref).abs() <= tol).all())
+        if one_sign:  # what one group of rows adds shows in some feature
+            m = 16 if N > 10000 else 1
+            at = torch.nonzero(pos[0] >= 0)[:, 0]
+            at = at[:at.numel() // m * m].view(-1, m)[:: max(1, N // (200 * m))].flatten()
+            t = _dw_terms(x[:1, at], cos, sin, pos[:1, at], g[:1, at], inter)[0]
+            last = t[:, (x.shape[2] - 1) // (512 // d) * (512 // d):].sum(1)  # the last group, not always full
+            assert bool((last.view(-1, m, d).sum(1).abs() > 2 * tol).any(-1).all())
+    if N == 37:  # the float64 sums themselves
+        for x, g in ((q, gq), (k, gk)):
+            ref = torch.from_numpy(S.norm_rope_backward(_f(x), np.ones(d), _f(cos), _f(sin), _f(g), pos.cpu().numpy(), 1e-6, inter)[1])
+            assert torch.allclose(_sums(x, cos, sin, pos, g, inter)[0].cpu(), ref, rtol=1e-12, atol=1e-12)
+
+
+@pytest.mark.gpu
+def test_gain_gradients_of_rows_beyond_32_bit_offsets():
+    """Rows at the start, across element 2^31 and at the end of 2.3e9; the others are zeros, which add exactly
+    nothing: their sums in float64."""
+    need_gpu()
+    N, H, d, n = 280000, 64, 128, 37
+    g = torch.Generator().manual_seed(27)
+    q = torch.zeros((1, N, H, d), dtype=BF, device="cuda")
+    k = torch.zeros((1, N, 1, d), dtype=BF, device="cuda")
+    cos, sin = fa.rope_tables(N, d)
+    w = (1 + 0.3 * torch.randn(d, generator=g)).cuda()
+    middle = 2 ** 31 // (H * d) - n // 2
+    rows = torch.cat([torch.arange(a, a + n) for a in (0, middle, N - n)]).cuda()
+    q[:, rows] = torch.randn((1, 3 * n, H, d), generator=g).to(BF).cuda()
+    k[:, rows] = torch.randn((1, 3 * n, 1, d), generator=g).to(BF).cuda()
+    gq, gk = fa.qk_norm_rope_fwd(q, k, cos, sin)
+    got = fa.qk_norm_rope_bwd(q, k, cos, sin, gq, gk, w, w)[2:]
+    for x, y, dw in ((q, gq, got[0]), (k, gk, got[1])):
+        ref, mag = _sums(x[:, rows], cos, sin, rows.view(1, -1), y[:, rows], False)
+        assert bool(((dw.double() - ref).abs() <= 2.0 ** -24 * ((3 * n * 16 + 39) * mag + ref.abs())).all())
+
+
+@pytest.mark.gpu
+def test_gain_gradients_where_one_output_is_used():
+    """Only k's output in the loss: its gain's gradient is the sum over k's rows, q's gain gets zeros."""
+    need_gpu()
+    q, k, cos, sin, w, pos, _, gk = _case(F32, 2, 9, 3, 2, 64, True, False, False, True, F32, seed=28)
+    k, wq, wk = (t.clone().requires_grad_(True) for t in (k, *w))
+    _, ko = fa.qk_norm_rope(q, k, cos, sin, wq, wk, pos)
+    dk, dwq, dwk = torch.autograd.grad(ko, (k, wq, wk), gk)
+    _check_bwd(k, wk, cos, sin, pos, False, gk, dk, dwk)
+    ref, mag = _sums(k.detach(), cos, sin, pos, gk, False)
+    assert bool(((dwk.double() - ref).abs() <= 2.0 ** -24 * ((_depth(q, k) + 32) * mag + ref.abs())).all())
+    assert torch.count_nonzero(dwq) == 0
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("inter", [False, True])
 def test_gradient_against_differences_of_the_kernel(inter):
