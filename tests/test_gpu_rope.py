@@ -529,6 +529,71 @@ def test_tables_rewritten_right_before_the_call(N, captured):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype,inter,d", [(BF, False, 128), (F32, True, 64)])
+def test_autograd_of_the_rotation_alone(dtype, inter, d):
+    need_gpu()
+    q, k, cos, sin, w, pos, gq, gk = _case(dtype, 2, 21, 5, 2, d, False, inter, True, False, F32, seed=29)
+    q, k = q.detach().requires_grad_(True), k.detach().requires_grad_(True)
+    qo, ko = fa.qk_norm_rope(q, k, cos, sin, interleaved=inter)
+    dq, dk = torch.autograd.grad((qo, ko), (q, k), (gq, gk))
+    _check_bwd(q, None, cos, sin, pos, inter, gq, dq, None)
+    _check_bwd(k, None, cos, sin, pos, inter, gk, dk, None)
+    with pytest.raises(RuntimeError):         # no second derivative here either
+        qo, _ = fa.qk_norm_rope(q, k, cos, sin, interleaved=inter)
+        dq, = torch.autograd.grad(qo.float().square().sum(), q, create_graph=True)
+        dq.sum().backward()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B,N,H,Hkv", [(0, 3, 2, 1), (2, 0, 2, 1), (2, 3, 0, 0), (2, 3, 0, 2)])
+@pytest.mark.parametrize("norm", [True, False])
+def test_autograd_of_empty_tensors(B, N, H, Hkv, norm):
+    need_gpu()
+    cos, sin = fa.rope_tables(4, 64)
+    leaves = [torch.ones((B, N, h, 64), device="cuda", requires_grad=True) for h in (H, Hkv)]
+    if norm:
+        leaves += [torch.ones(64, device="cuda", requires_grad=True) for _ in range(2)]
+    qo, ko = fa.qk_norm_rope(leaves[0], leaves[1], cos, sin, *leaves[2:])
+    (qo.sum() + ko.sum()).backward()
+    for t in leaves:
+        assert t.grad.shape == t.shape and torch.isfinite(t.grad).all()
+    if norm:
+        assert torch.count_nonzero(leaves[2].grad) == 0
+        assert (torch.count_nonzero(leaves[3].grad) > 0) == (B * N * Hkv > 0)
+
+
+@pytest.mark.gpu
+def test_a_training_step_captured():
+    """Forward and backward through autograd in one graph, replayed on new rows and gradients."""
+    need_gpu()
+    q, k, cos, sin, w, pos, gq, gk = _case(BF, 2, 40, 6, 2, 128, True, False, False, True, F32, seed=30)
+    new = _case(BF, 2, 40, 6, 2, 128, True, False, False, True, F32, seed=31)
+    want = [fa.qk_norm_rope_bwd(a, b, cos, sin, c, e, w[0], w[1], pos) for a, b, c, e in
+            ((q, k, gq, gk), (new[0], new[1], new[6], new[7]))]
+    leaves = [t.clone().requires_grad_(True) for t in (q, k, *w)]
+
+    def step():
+        qo, ko = fa.qk_norm_rope(leaves[0], leaves[1], cos, sin, leaves[2], leaves[3], pos)
+        return torch.autograd.grad((qo, ko), leaves, (gq, gk))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(out, want[0]))
+    with torch.no_grad():
+        for t, u in ((leaves[0], new[0]), (leaves[1], new[1]), (gq, new[6]), (gk, new[7])):
+            t.copy_(u)
+    graph.replay()
+    assert all(torch.equal(a, b) for a, b in zip(out, want[1]))
+
+
+@pytest.mark.gpu
 def test_captured_and_on_another_stream():
     """One graph of forward and backward, replayed on new inputs; and the calls on a side stream."""
     need_gpu()
