@@ -74,14 +74,17 @@ struct Here {
 };
 
 // The C call itself runs without the interpreter's lock where this thread holds it
-// (autograd's threads do not): a full launch queue would make it wait.
+// (autograd's threads do not): a full launch queue would make it wait.  The lock is taken back on
+// every way out: asking a tensor without storage (under vmap, say) for its pointer throws.
 template <typename F>
 int call_unlocked(F&& f) {
-  if (!PyGILState_Check()) return f();
-  PyThreadState* s = PyEval_SaveThread();
-  const int rc = f();
-  PyEval_RestoreThread(s);
-  return rc;
+  struct Unlocked {
+    PyThreadState* s = PyGILState_Check() ? PyEval_SaveThread() : nullptr;
+    ~Unlocked() {
+      if (s) PyEval_RestoreThread(s);
+    }
+  } unlocked;
+  return f();
 }
 
 // (batch, position, head) strides of a [B, N, heads, d] tensor whose features are contiguous

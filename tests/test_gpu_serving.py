@@ -169,6 +169,29 @@ def test_autograd_sees_what_the_calls_write():
 
 
 @pytest.mark.gpu
+def test_tensors_without_storage_are_refused():
+    """Under vmap and the other transforms of torch.func a tensor is a wrapper: an error, from every call."""
+    need_gpu()
+    cos, sin = fa.rope_tables(8, 64)
+    q, k = torch.randn(5, 2, 3, 4, 64, device="cuda").bfloat16(), torch.randn(5, 2, 3, 2, 64, device="cuda").bfloat16()
+    kc = torch.zeros(5, 4, 8, 2, 64, dtype=torch.uint8, device="cuda")
+    sc = torch.zeros(4, 2, 2, 8, dtype=torch.uint8, device="cuda")
+    table = torch.zeros(2, 2, dtype=torch.int32, device="cuda")
+    lens = torch.ones(2, dtype=torch.int32, device="cuda")
+    vmap = torch.func.vmap
+    for call in (lambda: vmap(lambda a, b: fa.qk_norm_rope(a, b, cos, sin))(q, k),
+                 lambda: vmap(lambda a, b: fa.qk_norm_rope_bwd(a, b, cos, sin, a, b)[:2])(q, k),
+                 lambda: vmap(lambda c: fa.cache_read(c, c, table, lens, 1, kv_scale=sc))(kc),
+                 lambda: vmap(lambda a: fa.cache_append(a, a, kc[0], kc[0], table, lens, kv_scale=sc))(k),
+                 lambda: vmap(lambda a: fa.decode_paged_fp8(a[:, 0].contiguous(), kc[0], kc[0], sc, table, lens))(q),
+                 lambda: torch.func.grad(lambda a: fa.qk_norm_rope(a, k[0], cos, sin)[0].float().sum())(q[0])):
+        with pytest.raises(RuntimeError):
+            call()
+    qo, _ = fa.qk_norm_rope(q[0], k[0], cos, sin)  # the interpreter and the binding are well
+    assert torch.isfinite(qo).all() and fa.last_device_status()[0] == 0
+
+
+@pytest.mark.gpu
 def test_two_graphs_and_an_eager_call_do_not_share_scratch():
     """Split decodes captured twice, replayed on two streams at once beside an eager one: each has partials of its own."""
     need_gpu()
