@@ -361,7 +361,9 @@ size_t fa_decode_workspace_size(int B, int H, int Hkv, int d, int page_size, int
  *   interleaved  0: pairs (i, i + d/2); 1: pairs (2i, 2i + 1).
  *   dtype, weight_dtype  FA_BF16 or FA_FP32 each; all arithmetic is fp32, each output is
  *                rounded once.
- *   d            64 or 128.  B * N < 2^31.
+ *   d            64 or 128 (FA_ERR_UNSUPPORTED otherwise).  B, H, Hkv <= 65535, N <= 2^22,
+ *                B * N < 2^31, fewer than 2^40 elements in a tensor (FA_ERR_TOO_LARGE
+ *                otherwise).
  */
 int fa_qk_norm_rope(const void* Q, const void* K, const void* q_weight, const void* k_weight, const float* cos_table,
                     const float* sin_table, const int* positions, void* Q_out, void* K_out, int B, int N, int H,
@@ -468,14 +470,14 @@ int fa_last_cuda_error(void);
  * Synchronises `stream`, then reads and clears the current device's status
  * word.  Returns FA_OK if no kernel reported a problem since the last call,
  * FA_ERR_DEVICE_INPUT if a kernel found device-side input out of range
- * (fa_decode_paged), FA_ERR_DEVICE_TIMEOUT if a bounded wait expired (the
+ * (the paged calls and fa_qk_norm_rope), FA_ERR_DEVICE_TIMEOUT if a bounded wait expired (the
  * affected launch's outputs are then undefined), FA_ERR_DEVICE_CHECK if a
  * kernel of the checking build (libfa_debug.so, compiled with FA_DEBUG) found
  * an index, coordinate or tensor-memory column outside its buffer (it skipped
  * that access; the launch's outputs are undefined), or FA_ERR_LAUNCH.  *detail
  * (if not NULL) receives the raw word: 0x1000 | the id of the wait that
  * expired, 0x2000 | the id of the failed input check (0xD1 a sequence
- * length, 0xD2 a page index), or 0x4000 | the id of the failed bounds check.
+ * length, 0xD2 a page index, 0xD3 a position), or 0x4000 | the id of the failed bounds check.
  * The first problem recorded wins.
  */
 int fa_last_device_status(void* stream, int* detail);

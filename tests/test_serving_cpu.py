@@ -181,6 +181,19 @@ def test_norm_rope_validation(L):
     assert back(wq=None, wk=None, dwq=None, dwk=None, N=0, ws=None, size=0) == 0
 
 
+def test_norm_rope_limits(L):
+    """The limits that the header states, from both sides (the pointers are refused next)."""
+    def call(B=1, N=4, H=2, Hkv=2, rows=1 << 23):
+        return L.fa_qk_norm_rope(None, None, None, None, None, None, None, None, None, B, N, H, Hkv, 64, None, None, rows,
+                                 0.0, 0, 0, 0, None)
+
+    for size, most in (("B", 65535), ("H", 65535), ("Hkv", 65535), ("N", 1 << 22)):
+        assert call(**{size: most}) == -1 and call(**{size: most + 1}) == -8, size
+    assert call(B=511, N=1 << 22) == -1 and call(B=512, N=1 << 22) == -8                      # B * N < 2^31
+    for size in ("H", "Hkv"):                                                                  # 2^40 elements
+        assert call(N=1 << 22, **{size: 4095}) == -1 and call(N=1 << 22, **{size: 4096}) == -8
+
+
 def test_cache_validation(L):
     def append(K=16, V=16, kc=16, vc=16, sc=16, bt=16, st=16, ct=None, B=2, N=3, Hkv=2, d=64, ks=None, vs=None, P=16,
                npg=10, mp=4, fp8=1):
