@@ -83,9 +83,9 @@ constexpr int kKShift = 20;
 // of it.  What a product loses is then below 2^(kVSpan - 34) of its own V row, however small that
 // is beside the others.  From the first scale outside on the products are sums of two bf16 terms,
 // which have fp32's range, and the unit follows the largest scale (up to 2^32, so that the range serves
-// both ways).
+// both ways).  A first token with V rows some 2^-7 of the others' stays inside.
 constexpr int kVUp = 4;
-constexpr int kVSpan = 10;
+constexpr int kVSpan = 14;
 constexpr int kVCap = 127 + 32;
 constexpr int kBarBytes = 192;
 

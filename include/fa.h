@@ -435,7 +435,7 @@ int fa_cache_read(const void* K_cache, const void* V_cache, const void* kv_scale
  * bytes of fa_cache_append (fp8 = 1).  The result is the exact attention of the
  * dequantised rows; sums and statistics are fp32.  Before P V the probabilities (of the
  * largest one so far) times the V scales are rounded: to f16 while the V scales of a
- * sequence's part differ little (2^-10 to 1 of 16 times the largest of the part's first 32
+ * sequence's part differ little (2^-14 to 1 of 16 times the largest of the part's first 32
  * rows), where a row whose product is below 2^-19 of the largest scale loses bits and below
  * 2^-30 counts as nothing; else to 16 bits with fp32's range.
  *   window_left  -1: every cached position is visible; else the query (the sequence's
