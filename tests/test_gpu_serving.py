@@ -192,6 +192,54 @@ def test_tensors_without_storage_are_refused():
 
 
 @pytest.mark.gpu
+def test_two_threads_on_streams_of_their_own():
+    """The calls give up the interpreter's lock: two threads run them at once, each on a stream that is not the
+    current one, with the results of one thread alone."""
+    import threading
+
+    need_gpu()
+    cos, sin = fa.rope_tables(4096, D)
+    w = torch.ones(D, dtype=torch.bfloat16, device="cuda")
+    length, steps = 3000, 40
+
+    def run(seed, stream, out):
+        try:
+            x = _projection(1, seed).expand(B, 1, H + 2 * HKV, D)
+            q, k, v = x.split((H, HKV, HKV), dim=2)
+            pages = (length + steps + PAGE) // PAGE
+            table = torch.arange(B * pages, dtype=torch.int32, device="cuda").view(B, pages)
+            kc, vc = (torch.full((B * pages, PAGE, HKV, D), 0x38, dtype=torch.uint8, device="cuda") for _ in range(2))
+            sc = torch.full((B * pages, HKV, 2, PAGE), 120, dtype=torch.uint8, device="cuda")
+            lens = [torch.full((B,), length + t, dtype=torch.int32, device="cuda") for t in range(steps + 1)]
+            torch.cuda.current_stream().synchronize()
+            got = []
+            for t in range(steps):
+                qr, kr = fa.qk_norm_rope_fwd(q, k, cos, sin, w, w, lens[t].view(B, 1), stream=stream)
+                fa.cache_append(kr, v, kc, vc, table, lens[t], kv_scale=sc, stream=stream)
+                got.append((*fa.decode_paged_fp8(qr.view(B, H, D), kc, vc, sc, table, lens[t + 1], stream=stream), kr))
+            got.append(fa.cache_read(kc, vc, table, lens[steps], length + steps, kv_scale=sc, stream=stream))
+            stream.synchronize()
+            out.append([y.cpu() for pair in got for y in pair])
+        except BaseException as e:  # noqa: BLE001 - handed to the test
+            out.append(e)
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    want = [[], []]
+    for i in range(2):
+        run(50 + i, streams[i], want[i])
+    got = [[], []]
+    threads = [threading.Thread(target=run, args=(50 + i, streams[i], got[i])) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for a, b in zip(want, got):
+        assert not isinstance(a[0], BaseException) and not isinstance(b[0], BaseException), (a[0], b[0])
+        assert len(a[0]) == len(b[0]) and all(torch.equal(x, y) for x, y in zip(a[0], b[0]))
+    assert fa.last_device_status()[0] == 0
+
+
+@pytest.mark.gpu
 def test_two_graphs_and_an_eager_call_do_not_share_scratch():
     """Split decodes captured twice, replayed on two streams at once beside an eager one: each has partials of its own."""
     need_gpu()
