@@ -552,6 +552,8 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None, window=
 
 # --------------------------------------------------------------------------
 # Around the attention: norm and rotation of query and key heads, the paged cache
+# (given outputs, workspaces and caches are written in place, which autograd is told;
+# one that requires a gradient is refused while gradients are recorded)
 # --------------------------------------------------------------------------
 _BINDING = None
 
@@ -596,8 +598,9 @@ def rope_tables(positions: int, d: int, base: float = 10000.0, device="cuda"):
 def qk_norm_rope(q, k, cos, sin, q_weight=None, k_weight=None, positions=None, eps: float = 1e-6,
                  interleaved: bool = False):
     """Differentiable ``qk_norm_rope_fwd`` (gradients of q, k and the gains; the tables get none; no forward-mode
-    derivative): the step before ``attention``.  As with any autograd function, capture its backward into a CUDA graph only while no eager graph of
-    the same leaves is alive (PyTorch accumulates into a leaf on the stream of the graph that saw it first)."""
+    derivative): the step before ``attention``.  As with any autograd function, capture its backward into a CUDA
+    graph only while no eager graph of the same leaves is alive (PyTorch accumulates into a leaf on the stream of
+    the graph that saw it first)."""
     return _native().norm_rope(q, k, cos, sin, q_weight, k_weight, positions, eps, interleaved)
 
 
